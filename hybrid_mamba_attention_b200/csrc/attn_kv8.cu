@@ -1,0 +1,306 @@
+// Paged block attention over the 8-bit KV cache (hspec_attn_paged_block_kv8): the
+// CUDA-core split kernel for any shape, the split policy, and the merge of the partials.
+//
+// attn_kv8_split_kernel: one CTA per (split, kv head g and block of 32 query rows,
+// request c).  Its rows are (position j, query head g*G + i) pairs, all reading kv head
+// g.  Keys and values pass through shared memory in tiles of 32, dequantised to fp32
+// (code * scale is exact there); a warp owns four rows: lane t computes the four dot
+// products of key t, the online softmax (exp2 domain) reduces over the lanes, and for
+// the product with V a lane owns the dims t, t + 32, ...  Hidden keys are skipped, not
+// multiplied by zero, so that a NaN in one reaches no row that does not see it.
+//
+// attn_kv8_merge_kernel: W = 1, 2, 4 or 8 warps per output row combine its partials,
+// o = sum_s 2^(m_s - M) acc_s / sum_s 2^(m_s - M) l_s, in a fixed order.
+#include "../../include/hspec.h"
+#include "common.cuh"
+#include "kernels.cuh"
+#include "kv8.cuh"
+
+namespace hspec {
+
+int* device_error_word();
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 32;              // query rows per CTA
+constexpr int RW = kRows / kWarps;     // rows per warp
+constexpr int kTile = 32;              // keys per tile
+constexpr int kMaxDpl = 8;             // dims per lane (head_dim <= 256)
+
+// Shared memory in floats: q [32][Dp], k [32][Dp + 4] (a lane per key reads float4s: the
+// four extra words put the lanes on different banks), v [32][Dp], p [8][RW][32].
+__host__ __device__ inline int dim_pad(int D) { return (D + 3) & ~3; }
+inline size_t split_smem(int D) {
+  const int Dp = dim_pad(D);
+  return (size_t)(kRows * Dp + kTile * (Dp + 4) + kTile * Dp + kRows * kTile) * sizeof(float);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) attn_kv8_split_kernel(const AttnKv8Args a, float scale_log2) {
+  extern __shared__ float4 sm4[];
+  float* sm = (float*)sm4;
+  const int D = a.kv.D, Dp = dim_pad(D), Hkv = a.kv.Hkv, page = a.kv.page_size;
+  float* sQ = sm;
+  float* sK = sQ + kRows * Dp;
+  float* sV = sK + kTile * (Dp + 4);
+  float* sP = sV + kTile * Dp;
+  const int split = blockIdx.x, g = blockIdx.y % Hkv, rb = blockIdx.y / Hkv, c = blockIdx.z;
+  const int G = a.Hq / Hkv, R = a.K * G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ctx = a.ctx_lens[c];
+  if (ctx < 0 || ctx > (long)a.kv.max_pages * page) {
+    if (threadIdx.x == 0) flag_error(a.err, kErrCtxOOB);
+    return;
+  }
+  const int total = ctx + (a.kb ? a.K : 0);
+  const int t_begin = split * a.split_tokens;
+  if (t_begin >= total) return;  // the merge reads only the splits that hold tokens
+  const int t_end = min(total, t_begin + a.split_tokens);
+
+  for (int i = threadIdx.x; i < kRows * Dp; i += kThreads) {
+    const int r = rb * kRows + i / Dp, e = i % Dp;
+    float v = 0.f;
+    if (r < R && e < D)
+      v = to_f(((const T*)a.q)[(size_t)(c * a.K + r / G) * a.q_rs + (size_t)(g * G + r % G) * D + e]) * scale_log2;
+    sQ[i] = v;
+  }
+  // keys [0, vis) are seen by the row
+  int vis[RW];
+  float m[RW], l[RW], acc[RW][kMaxDpl];
+#pragma unroll
+  for (int r = 0; r < RW; ++r) {
+    const int row = rb * kRows + warp * RW + r, j = row / G;
+    vis[r] = row >= R ? 0 : !a.causal ? total : a.kb ? ctx + j + 1 : ctx - (a.K - 1) + j;
+    m[r] = -INFINITY, l[r] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxDpl; ++i) acc[r][i] = 0.f;
+  }
+  const int32_t* table = a.kv.table + (size_t)c * a.kv.max_pages;
+
+  for (int t0 = t_begin; t0 < t_end; t0 += kTile) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTile * Dp; i += kThreads) {
+      const int tt = i / Dp, e = i % Dp, t = t0 + tt;
+      float k = 0.f, v = 0.f;
+      if (e < D && t < t_end) {
+        if (t < ctx) {
+          const int pg = table[t / page];
+          if (pg >= 0 && pg < a.kv.num_pages) {
+            const size_t ph = (size_t)pg * Hkv + g, off = (ph * page + t % page) * D + e;
+            k = e4m3_to_f(a.kv.k[off]) * a.kv.ks[ph];
+            v = e4m3_to_f(a.kv.v[off]) * a.kv.vs[ph];
+          } else if (e == 0) {
+            flag_error(a.err, kErrPageOOB);
+          }
+        } else {
+          const size_t row = (size_t)(c * a.K + (t - ctx));
+          k = to_f(((const T*)a.kb)[row * a.kb_rs + (size_t)g * D + e]);
+          v = to_f(((const T*)a.vb)[row * a.vb_rs + (size_t)g * D + e]);
+        }
+      }
+      sK[tt * (Dp + 4) + e] = k;
+      sV[tt * Dp + e] = v;
+    }
+    __syncthreads();
+    float s[RW];
+#pragma unroll
+    for (int r = 0; r < RW; ++r) s[r] = 0.f;
+    for (int e = 0; e < Dp; e += 4) {
+      const float4 k = *(const float4*)(sK + lane * (Dp + 4) + e);
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        const float4 q = *(const float4*)(sQ + (warp * RW + r) * Dp + e);
+        s[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[r]))));
+      }
+    }
+    int nv[RW];
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      nv[r] = min(max(min(vis[r], t_end) - t0, 0), kTile);  // keys of the tile that the row sees
+      const float sc = lane < nv[r] ? s[r] : -INFINITY;
+      const float m_new = fmaxf(m[r], warp_max(sc));
+      // with nothing visible yet (or NaN alone) subtract 0: a masked weight is 0, not NaN
+      const float base = m_new == -INFINITY ? 0.f : m_new;
+      const float p = lane < nv[r] ? exp2f(sc - base) : 0.f;
+      const float alpha = m[r] == -INFINITY ? (l[r] == 0.f ? 0.f : 1.f) : exp2f(m[r] - m_new);
+      l[r] = l[r] * alpha + warp_sum(p);
+      m[r] = m_new;
+#pragma unroll
+      for (int i = 0; i < kMaxDpl; ++i) acc[r][i] *= alpha;
+      sP[(warp * RW + r) * kTile + lane] = p;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kMaxDpl; ++i) {
+      const int e = lane + 32 * i;
+      if (e >= D) break;
+      for (int t = 0; t < kTile; ++t) {
+        const float v = sV[t * Dp + e];
+#pragma unroll
+        for (int r = 0; r < RW; ++r)
+          if (t < nv[r]) acc[r][i] = fmaf(sP[(warp * RW + r) * kTile + t], v, acc[r][i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RW; ++r) {
+    const int row = rb * kRows + warp * RW + r;
+    if (row >= R) break;
+    const size_t base = (((size_t)c * Hkv + g) * a.n_splits + split) * R + row;
+#pragma unroll
+    for (int i = 0; i < kMaxDpl; ++i)
+      if (lane + 32 * i < D) a.ws_acc[base * D + lane + 32 * i] = acc[r][i];
+    if (lane == 0) {
+      a.ws_ml[base * 2] = m[r];
+      a.ws_ml[base * 2 + 1] = l[r];
+    }
+  }
+}
+
+// W warps per row; lane t holds the dims t + 32 i, i < E.
+template <typename T, int W, int E>
+__global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const AttnKv8Args a) {
+  constexpr int RPC = 8 / W;  // rows per CTA
+  __shared__ float s_acc[W > 1 ? 8 : 1][32 * E];
+  __shared__ float s_ml[8][2];
+  const int D = a.kv.D, Hkv = a.kv.Hkv;
+  const int wib = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wq = wib % W, rl = wib / W;
+  const int G = a.Hq / Hkv, R = a.K * G;
+  const long rows = (long)a.C * a.K * a.Hq;
+  const long row_id = (long)blockIdx.x * RPC + rl;
+  const bool live = row_id < rows;
+  const long rid = live ? row_id : 0;
+  const int h = (int)(rid % a.Hq), j = (int)(rid / a.Hq % a.K), c = (int)(rid / a.Hq / a.K);
+  const int g = h / G, row = j * G + h % G;
+  const int ctx = a.ctx_lens[c];
+  const bool valid = live && ctx >= 0 && ctx <= (long)a.kv.max_pages * a.kv.page_size;
+  const int ns = valid ? (ctx + (a.kb ? a.K : 0) + a.split_tokens - 1) / a.split_tokens : 0;
+  const size_t base0 = ((size_t)c * Hkv + g) * a.n_splits * R + row, stride = R;
+  float M = -INFINITY, L = 0.f, o[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) o[i] = 0.f;
+  auto fold = [&](float m, float l, auto acc_of) {
+    if (l == 0.f) return;  // no key seen
+    const float mn = fmaxf(M, m);
+    const float sc = L == 0.f ? 0.f : exp2f(M - mn), w = exp2f(m - mn);
+    L = L * sc + l * w;
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] = o[i] * sc + acc_of(i) * w;
+    M = mn;
+  };
+  for (int q = wq; q < ns; q += W) {
+    const size_t b = base0 + (size_t)q * stride;
+    const float2 ml = *(const float2*)(a.ws_ml + b * 2);
+    const float* acc = a.ws_acc + b * D;
+    fold(ml.x, ml.y, [&](int i) { return lane + 32 * i < D ? acc[lane + 32 * i] : 0.f; });
+  }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) s_acc[wib][lane + 32 * i] = o[i];
+    if (lane == 0) s_ml[wib][0] = M, s_ml[wib][1] = L;
+    __syncthreads();
+    if (wq != 0) return;
+    for (int w = 1; w < W; ++w)
+      fold(s_ml[wib + w][0], s_ml[wib + w][1], [&](int i) { return s_acc[wib + w][lane + 32 * i]; });
+  }
+  if (!live) return;
+  T* out = (T*)a.out + (size_t)(c * a.K + j) * a.o_rs + (size_t)h * D;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    if (lane + 32 * i < D) out[lane + 32 * i] = from_f<T>(o[i] * inv);
+}
+
+template <typename T, int W>
+void launch_merge_w(const AttnKv8Args& a, long rows, cudaStream_t s) {
+  const int grid = (int)((rows + 8 / W - 1) / (8 / W));
+  if (a.kv.D <= 128) attn_kv8_merge_kernel<T, W, 4><<<grid, 256, 0, s>>>(a);
+  else attn_kv8_merge_kernel<T, W, 8><<<grid, 256, 0, s>>>(a);
+  note_launch();
+}
+
+template <typename T>
+void launch_merge(const AttnKv8Args& a, cudaStream_t s) {
+  // warps per output row: enough warps in all for about 32 per SM
+  const long rows = (long)a.C * a.K * a.Hq;
+  int W = 1;
+  while (W < 8 && rows * W < 148L * 32) W *= 2;
+  switch (W) {
+    case 1: launch_merge_w<T, 1>(a, rows, s); break;
+    case 2: launch_merge_w<T, 2>(a, rows, s); break;
+    case 4: launch_merge_w<T, 4>(a, rows, s); break;
+    default: launch_merge_w<T, 8>(a, rows, s); break;
+  }
+}
+
+template <typename T>
+bool launch_split(const AttnKv8Args& a, cudaStream_t s) {
+  const size_t smem = split_smem(a.kv.D);
+  if (cudaFuncSetAttribute(attn_kv8_split_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+      cudaSuccess) {
+    set_error("cudaFuncSetAttribute(attn_kv8_split_kernel) failed");
+    return false;
+  }
+  const int nrb = cdiv((long)a.K * (a.Hq / a.kv.Hkv), kRows);
+  const float scale_log2 = 1.4426950408889634f / sqrtf((float)a.kv.D);
+  attn_kv8_split_kernel<T><<<dim3(a.n_splits, a.kv.Hkv * nrb, a.C), kThreads, smem, s>>>(a, scale_log2);
+  note_launch();
+  return true;
+}
+
+// CUDA-core path: tokens per split (a requested length, or about 16 CTAs per SM at the
+// table's full width) and splits per sequence.
+struct Split {
+  int tokens, n;
+};
+Split split_of(int C, int K, int G, const Kv8& kv, int req) {
+  const long max_keys = (long)kv.max_pages * kv.page_size + K;
+  const long nrb = cdiv((long)K * G, kRows);
+  long per = req > 0 ? req : ((long)C * kv.Hkv * nrb * max_keys + 148L * 16 - 1) / (148L * 16);
+  per = ((per + 63) / 64) * 64;
+  if (per < 64) per = 64;
+  // the grid's x extent holds the splits: no limit in reach (2^31), so any length works
+  return {(int)(per < max_keys ? per : max_keys), (int)((max_keys + per - 1) / per)};
+}
+
+}  // namespace
+
+bool attn_kv8_supported(int K, int G, int D, const char** why) {
+  if (K < 1 || K > 64) return *why = "K must be in 1..64", false;
+  if (D > 256) return *why = "head_dim must be <= 256", false;
+  if ((long)K * G > 65536) return *why = "K * Hq / Hkv must be <= 65536", false;
+  return true;
+}
+
+size_t attn_kv8_ws_bytes(int dtype, int C, int K, int G, const Kv8& kv, int split_req) {
+  (void)dtype;
+  const Split sp = split_of(C, K, G, kv, split_req);
+  const size_t rows = (size_t)C * kv.Hkv * sp.n * K * G;
+  return rows * (kv.D + 2) * sizeof(float);
+}
+
+bool attn_kv8(int dtype, AttnKv8Args& a, int split_req, void* ws, cudaStream_t s) {
+  const int G = a.Hq / a.kv.Hkv;
+  const Split sp = split_of(a.C, a.K, G, a.kv, split_req);
+  if (a.C > 65535 || (long)a.kv.Hkv * cdiv((long)a.K * G, kRows) > 65535) {
+    set_error("attention over the 8-bit cache: too many requests or heads");
+    return false;
+  }
+  a.split_tokens = sp.tokens, a.n_splits = sp.n;
+  const size_t rows = (size_t)a.C * a.kv.Hkv * sp.n * a.K * G;
+  a.ws_acc = (float*)ws;
+  a.ws_ml = a.ws_acc + rows * a.kv.D;
+  if (dtype == HSPEC_DTYPE_BF16) {
+    if (!launch_split<bf16>(a, s)) return false;
+    launch_merge<bf16>(a, s);
+  } else {
+    if (!launch_split<float>(a, s)) return false;
+    launch_merge<float>(a, s);
+  }
+  return true;
+}
+
+}  // namespace hspec

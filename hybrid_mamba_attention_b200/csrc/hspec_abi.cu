@@ -244,6 +244,55 @@ hspec_status validate_kv(const hspec_cfg* c, const hspec_kv_view* kv) {
   return HSPEC_OK;
 }
 
+hspec_status validate_kv8(const hspec_cfg* c, const hspec_kv8_view* kv) {
+  if (!kv) FAIL(HSPEC_ERR_INVALID_ARG, "kv8 view is NULL");
+  if (!kv->k_codes || !kv->v_codes || !kv->k_scales || !kv->v_scales || !kv->page_table)
+    FAIL(HSPEC_ERR_INVALID_ARG, "kv8 codes, scales and page table must be non-NULL");
+  if (((uintptr_t)kv->k_codes | (uintptr_t)kv->v_codes) & 15)
+    FAIL(HSPEC_ERR_INVALID_ARG, "kv8 codes must be 16-byte aligned");
+  if (kv->num_pages <= 0 || kv->max_pages <= 0)
+    FAIL(HSPEC_ERR_PAGE_OOB, "num_pages (%d) and max_pages (%d) must be positive", kv->num_pages, kv->max_pages);
+  if ((long)kv->max_pages * c->page_size > (1L << 30))
+    FAIL(HSPEC_ERR_UNSUPPORTED, "max_pages * page_size exceeds 2^30 tokens");
+  return HSPEC_OK;
+}
+
+Kv8 kv8_of(const hspec_cfg* c, const hspec_kv8_view* kv) {
+  return {(uint8_t*)kv->k_codes, (uint8_t*)kv->v_codes, kv->k_scales, kv->v_scales, kv->page_table,
+          kv->num_pages, kv->max_pages, c->page_size, c->n_kv_heads, c->head_dim};
+}
+
+// The write's and the read's arguments, checked.
+hspec_status kv8_move_args(const hspec_cfg* c, const hspec_kv8_view* kv, const void* k, const void* v,
+                           long long row_stride, const int32_t* cu, const int32_t* first, int C, int T,
+                           Kv8MoveArgs* a) {
+  hspec_status st = validate_cfg(c, true, false);
+  if (st) return st;
+  if ((st = validate_kv8(c, kv))) return st;
+  if (!cu || (T > 0 && (!k || !v))) FAIL(HSPEC_ERR_INVALID_ARG, "the rows and their offsets must be non-NULL");
+  if (C < 1 || T < 0) FAIL(HSPEC_ERR_INVALID_ARG, "C=%d T=%d (need C >= 1, T >= 0)", C, T);
+  if (T > 1 << 30 || C > 1 << 28 || c->n_kv_heads > 32767)
+    FAIL(HSPEC_ERR_UNSUPPORTED, "more than 2^30 rows, 2^28 requests or 32767 kv heads");
+  const long long row = (long long)c->n_kv_heads * c->head_dim;
+  if (row_stride != 0 && row_stride < row)
+    FAIL(HSPEC_ERR_INVALID_ARG, "row_stride %lld is below Hkv * head_dim = %lld", row_stride, row);
+  *a = {kv8_of(c, kv), const_cast<void*>(k), const_cast<void*>(v), (long)(row_stride ? row_stride : row), cu, first,
+        C, T, device_error_word()};
+  return HSPEC_OK;
+}
+
+// Attention over the 8-bit cache: what every launch of a call shares.
+AttnKv8Args attn_kv8_args(const hspec_cfg* c, const hspec_kv8_view* kv, const int32_t* ctx_lens, int C, int K) {
+  AttnKv8Args a = {};
+  a.kv = kv8_of(c, kv);
+  a.C = C, a.K = K, a.Hq = c->n_q_heads;
+  a.ctx_lens = ctx_lens;
+  a.causal = (c->flags & HSPEC_FLAG_CAUSAL_BLOCK) != 0;
+  a.err = device_error_word();
+  a.wait_ns = wait_ns(c);
+  return a;
+}
+
 struct AttnPlan {
   int split_tokens, n_splits, max_chunks;
   size_t rows;  // partial rows
@@ -559,6 +608,64 @@ hspec_status hspec_attn_paged_block(const hspec_cfg* cfg, const void* q, const h
   a.out = out, a.o_rs = qrow;
   if (!attn_paged(cfg->dtype, a, (cudaStream_t)stream)) return HSPEC_ERR_UNSUPPORTED;
   return check_launch("hspec_attn_paged_block");
+}
+
+hspec_status hspec_kv8_write(const hspec_cfg* cfg, const void* k_new, const void* v_new, long long row_stride,
+                             const int32_t* cu_new, const int32_t* first, int C, int T, const hspec_kv8_view* kv,
+                             void* stream) {
+  Kv8MoveArgs a;
+  hspec_status st = kv8_move_args(cfg, kv, k_new, v_new, row_stride, cu_new, first, C, T, &a);
+  if (st) return st;
+  if (!first) FAIL(HSPEC_ERR_INVALID_ARG, "first is NULL");
+  if (T == 0) return HSPEC_OK;
+  kv8_write(cfg->dtype, a, (cudaStream_t)stream);
+  return check_launch("hspec_kv8_write");
+}
+
+hspec_status hspec_kv8_read(const hspec_cfg* cfg, const hspec_kv8_view* kv, const int32_t* cu, const int32_t* first,
+                            int C, int T, void* k_out, void* v_out, long long row_stride, void* stream) {
+  Kv8MoveArgs a;
+  hspec_status st = kv8_move_args(cfg, kv, k_out, v_out, row_stride, cu, first, C, T, &a);
+  if (st) return st;
+  if (T == 0) return HSPEC_OK;
+  kv8_read(cfg->dtype, a, (cudaStream_t)stream);
+  return check_launch("hspec_kv8_read");
+}
+
+size_t hspec_attn_kv8_workspace_size(const hspec_cfg* cfg, int C, int K, int max_pages) {
+  if (validate_cfg(cfg, true, false) || C < 1 || K < 1 || K > 64 || max_pages < 1) return 0;
+  if ((long)max_pages * cfg->page_size > (1L << 30)) return 0;
+  hspec_kv8_view kv = {};
+  kv.max_pages = max_pages;
+  return align256(attn_kv8_ws_bytes(cfg->dtype, C, K, cfg->n_q_heads / cfg->n_kv_heads, kv8_of(cfg, &kv),
+                                    cfg->attn_split_tokens));
+}
+
+hspec_status hspec_attn_paged_block_kv8(const hspec_cfg* cfg, const void* q, const hspec_kv8_view* kv,
+                                        const int32_t* ctx_lens, const void* k_blk, const void* v_blk, int C, int K,
+                                        void* out, void* workspace, size_t ws_bytes, void* stream) {
+  hspec_status st = validate_cfg(cfg, true, false);
+  if (st) return st;
+  if ((st = validate_kv8(cfg, kv))) return st;
+  if (!q || !ctx_lens || !out) FAIL(HSPEC_ERR_INVALID_ARG, "q, ctx_lens and out must be non-NULL");
+  if (!k_blk != !v_blk) FAIL(HSPEC_ERR_INVALID_ARG, "k_blk and v_blk must both be given or both be NULL");
+  if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)k_blk | (uintptr_t)v_blk) & 15)
+    FAIL(HSPEC_ERR_INVALID_ARG, "q, out, k_blk and v_blk must be 16-byte aligned");
+  if (C < 1 || K < 1 || K > 64) FAIL(HSPEC_ERR_UNSUPPORTED, "C=%d K=%d (need C >= 1, 1 <= K <= 64)", C, K);
+  const char* why = "";
+  if (!attn_kv8_supported(K, cfg->n_q_heads / cfg->n_kv_heads, cfg->head_dim, &why))
+    FAIL(HSPEC_ERR_UNSUPPORTED, "attention over the 8-bit cache: %s", why);
+  const size_t need = hspec_attn_kv8_workspace_size(cfg, C, K, kv->max_pages);
+  if (!workspace || ((uintptr_t)workspace & 255) || ws_bytes < need)
+    FAIL(HSPEC_ERR_WORKSPACE, "attention needs a 256-byte aligned workspace of %zu bytes (got %zu)", need, ws_bytes);
+  AttnKv8Args a = attn_kv8_args(cfg, kv, ctx_lens, C, K);
+  const long qrow = (long)cfg->n_q_heads * cfg->head_dim, krow = (long)cfg->n_kv_heads * cfg->head_dim;
+  a.q = q, a.q_rs = qrow;
+  a.kb = k_blk, a.kb_rs = krow;
+  a.vb = v_blk, a.vb_rs = krow;
+  a.out = out, a.o_rs = qrow;
+  if (!attn_kv8(cfg->dtype, a, cfg->attn_split_tokens, workspace, (cudaStream_t)stream)) return HSPEC_ERR_UNSUPPORTED;
+  return check_launch("hspec_attn_paged_block_kv8");
 }
 
 size_t hspec_verify_workspace_size(const hspec_cfg* cfg, int C, int K) {

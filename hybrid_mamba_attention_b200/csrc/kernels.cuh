@@ -177,4 +177,43 @@ size_t verify_ws_bytes(int dtype, int C, int K, int V);
 void verify_greedy(int dtype, const void* logits, int V, const int32_t* drafts, int C, int K,
                    int32_t* accepted, int32_t* next_token, int32_t* ctx_lens, void* ws, cudaStream_t s);
 
+// ------------------------------------------------------------ kv8.cu
+// The 8-bit paged cache (hspec_kv8_view) as the kernels take it.
+struct Kv8 {
+  uint8_t* k; uint8_t* v;      // e4m3 codes [num_pages, Hkv, page_size, D]
+  float* ks; float* vs;        // scales [num_pages, Hkv]
+  const int32_t* table;        // [C, max_pages]
+  int num_pages, max_pages, page_size, Hkv, D;
+};
+struct Kv8MoveArgs {
+  Kv8 kv;
+  void* k; void* v; long rs;   // rows [T, Hkv, D] (dtype), row stride in elements
+  const int32_t* cu;           // [C + 1]
+  const int32_t* first;        // [C] or NULL (0)
+  int C, T;
+  int* err;
+};
+void kv8_write(int dtype, const Kv8MoveArgs& a, cudaStream_t s);
+void kv8_read(int dtype, const Kv8MoveArgs& a, cudaStream_t s);
+
+// ------------------------------------------------------------ attn_kv8.cu
+struct AttnKv8Args {
+  Kv8 kv;
+  int C, K, Hq;
+  const void* q; long q_rs;    // token row stride; head h at column h*D
+  const void* kb; long kb_rs;  // block keys / values, kv head g at column g*D (NULL: cache only)
+  const void* vb; long vb_rs;
+  void* out; long o_rs;
+  const int32_t* ctx_lens;
+  bool causal;
+  int split_tokens, n_splits;  // CUDA-core path: tokens per split, splits per sequence (upper bound)
+  float* ws_acc; float* ws_ml; // partials
+  int* err;
+  unsigned long long wait_ns;  // pipeline waits give up after this long (0: the default)
+};
+bool attn_kv8_supported(int K, int G, int D, const char** why);
+size_t attn_kv8_ws_bytes(int dtype, int C, int K, int G, const Kv8& kv, int split_req);
+// Fills the workspace fields and launches; false (message recorded) if it cannot.
+bool attn_kv8(int dtype, AttnKv8Args& a, int split_req, void* ws, cudaStream_t s);
+
 }  // namespace hspec

@@ -37,7 +37,8 @@ EXPORTS = ("hspec_inject_state", "hspec_ssd_block_scan", "hspec_attn_workspace_s
            "hspec_step_workspace_size", "hspec_draft_step", "hspec_sync_status",
            "hspec_status_string", "hspec_last_error", "hspec_launch_count", "hspec_version",
            "hspec_profile_enable", "hspec_profile_read", "hspec_attn_paged_block_noalloc",
-           "hspec_verify_workspace_size", "hspec_verify_greedy")
+           "hspec_verify_workspace_size", "hspec_verify_greedy",
+           "hspec_kv8_write", "hspec_kv8_read", "hspec_attn_kv8_workspace_size", "hspec_attn_paged_block_kv8")
 HSPEC_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -75,6 +76,12 @@ class hspec_kv_view(ct.Structure):
                 ("page_table", ct.c_void_p), ("max_pages", ct.c_int)]
 
 
+class hspec_kv8_view(ct.Structure):
+    _fields_ = [("k_codes", ct.c_void_p), ("v_codes", ct.c_void_p), ("k_scales", ct.c_void_p),
+                ("v_scales", ct.c_void_p), ("num_pages", ct.c_int), ("page_table", ct.c_void_p),
+                ("max_pages", ct.c_int)]
+
+
 class hspec_step_in(ct.Structure):
     _fields_ = [("C", ct.c_int), ("K", ct.c_int), ("tokens", ct.c_void_p), ("x_in", ct.c_void_p),
                 ("h_last", ct.c_void_p), ("ctx_lens", ct.c_void_p),
@@ -91,7 +98,7 @@ class hspec_step_out(ct.Structure):
 def _load():
     path = _build.build()
     lib = ct.CDLL(path)
-    P, I, Z, V = ct.c_void_p, ct.c_int, ct.c_size_t, ct.c_void_p
+    P, I, Z, V, L = ct.c_void_p, ct.c_int, ct.c_size_t, ct.c_void_p, ct.c_longlong
     cfgp = ct.POINTER(hspec_cfg)
     sig = {
         "hspec_inject_state": (I, [cfgp, P, P, I, P, V]),
@@ -110,6 +117,10 @@ def _load():
         "hspec_profile_enable": (I, [I]),
         "hspec_profile_read": (I, [P, P, P, I]),
         "hspec_attn_paged_block_noalloc": (I, [cfgp, P, ct.POINTER(hspec_kv_view), P, P, P, I, I, P, V]),
+        "hspec_kv8_write": (I, [cfgp, P, P, L, P, P, I, I, ct.POINTER(hspec_kv8_view), V]),
+        "hspec_kv8_read": (I, [cfgp, ct.POINTER(hspec_kv8_view), P, P, I, I, P, P, L, V]),
+        "hspec_attn_kv8_workspace_size": (Z, [cfgp, I, I, I]),
+        "hspec_attn_paged_block_kv8": (I, [cfgp, P, ct.POINTER(hspec_kv8_view), P, P, P, I, I, P, P, Z, V]),
         "hspec_verify_workspace_size": (Z, [cfgp, I, I]),
         "hspec_verify_greedy": (I, [cfgp, P, P, I, I, P, P, P, P, Z, V]),
     }
@@ -170,6 +181,15 @@ def kv_view(cache: dict) -> hspec_kv_view:
                          max_pages=int(cache["page_table"].shape[1]))
 
 
+def kv8_view(cache: dict) -> hspec_kv8_view:
+    """hspec_kv8_view of an 8-bit cache dict: k_codes, v_codes [num_pages, Hkv, page, D]
+    (one byte each), k_scales, v_scales [num_pages, Hkv] fp32, page_table."""
+    return hspec_kv8_view(k_codes=_ptr(cache["k_codes"]), v_codes=_ptr(cache["v_codes"]),
+                          k_scales=_ptr(cache["k_scales"]), v_scales=_ptr(cache["v_scales"]),
+                          num_pages=int(cache["k_codes"].shape[0]), page_table=_ptr(cache["page_table"]),
+                          max_pages=int(cache["page_table"].shape[1]))
+
+
 def alloc_workspace(nbytes: int, device=None) -> torch.Tensor:
     """A 256-byte aligned device buffer (torch's caching allocator aligns to 512)."""
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
@@ -228,6 +248,45 @@ def hspec_attn_paged_block_noalloc(cfg: hspec_cfg, q, kv: hspec_kv_view, ctx_len
     _check(_lib.hspec_attn_paged_block_noalloc(ct.byref(cfg), _ptr(q), ct.byref(kv), _ptr(ctx_lens), _ptr(k_blk),
                                                _ptr(v_blk), C, K, _ptr(out), _stream(stream)),
            "hspec_attn_paged_block_noalloc")
+
+
+def _row_stride(rows, mate, D: int) -> int:
+    """Elements between the rows of [T, Hkv, D] tensors (a slice of a wider projection's
+    output will do), each row's heads dense."""
+    dense = rows.stride(2) == 1 and (rows.shape[1] == 1 or rows.stride(1) == D)
+    if not dense or rows.shape != mate.shape or rows.stride() != mate.stride():
+        raise ValueError("k and v rows must be [T, Hkv, D] of the same strides, each row dense")
+    return int(rows.stride(0)) if rows.shape[0] > 1 else 0
+
+
+def hspec_kv8_write(cfg: hspec_cfg, k_new, v_new, cu_new, first, kv: hspec_kv8_view, stream=None):
+    """Quantises rows cu_new[c] .. cu_new[c + 1] - 1 of k_new, v_new [T, Hkv, D] (cfg dtype)
+    into the 8-bit cache as tokens first[c], first[c] + 1, ... of request c."""
+    _check(_lib.hspec_kv8_write(ct.byref(cfg), _ptr(k_new), _ptr(v_new), _row_stride(k_new, v_new, cfg.head_dim),
+                                _ptr(cu_new), _ptr(first), int(cu_new.shape[0]) - 1, int(k_new.shape[0]),
+                                ct.byref(kv), _stream(stream)), "hspec_kv8_write")
+
+
+def hspec_kv8_read(cfg: hspec_cfg, kv: hspec_kv8_view, cu, first, k_out, v_out, stream=None):
+    """Reads tokens first[c] .. of request c (first None: from 0) into rows cu[c] ..
+    cu[c + 1] - 1 of k_out, v_out [T, Hkv, D] (cfg dtype)."""
+    _check(_lib.hspec_kv8_read(ct.byref(cfg), ct.byref(kv), _ptr(cu), _ptr(first), int(cu.shape[0]) - 1,
+                               int(k_out.shape[0]), _ptr(k_out), _ptr(v_out),
+                               _row_stride(k_out, v_out, cfg.head_dim), _stream(stream)), "hspec_kv8_read")
+
+
+def hspec_attn_kv8_workspace_size(cfg: hspec_cfg, C: int, K: int, max_pages: int) -> int:
+    return int(_lib.hspec_attn_kv8_workspace_size(ct.byref(cfg), C, K, max_pages))
+
+
+def hspec_attn_paged_block_kv8(cfg: hspec_cfg, q, kv: hspec_kv8_view, ctx_lens, k_blk, v_blk, out, workspace,
+                               stream=None):
+    """Block attention over the 8-bit cache; k_blk = v_blk = None: over the cache alone."""
+    C, K = int(q.shape[0]), int(q.shape[1])
+    _check(_lib.hspec_attn_paged_block_kv8(ct.byref(cfg), _ptr(q), ct.byref(kv), _ptr(ctx_lens), _ptr(k_blk),
+                                           _ptr(v_blk), C, K, _ptr(out), _ptr(workspace),
+                                           workspace.numel() * workspace.element_size(), _stream(stream)),
+           "hspec_attn_paged_block_kv8")
 
 
 def hspec_drafter_create(cfg: hspec_cfg, weights: hspec_model_weights) -> ct.c_void_p:

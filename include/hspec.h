@@ -231,6 +231,86 @@ HSPEC_API hspec_status hspec_attn_paged_block_noalloc(const hspec_cfg* cfg, cons
                                                       const void* k_blk, const void* v_blk, int C, int K,
                                                       void* out, void* stream);
 
+/* ------------------------------------------------------- 8-bit paged KV cache
+ * A target that keeps its keys and values in 8 bits: e4m3 codes (1 sign, 4 exponent
+ * and 3 fraction bits, largest value 448, no infinity, NaN = 0x7F / 0xFF) with one fp32
+ * scale for each page and kv head, K and V apart; a value is code * scale.  Codes of a
+ * page and head are contiguous (head-major pages), unlike the pools of hspec_kv_view.
+ *
+ * hspec_kv8_write() chooses scale(page, head) = 0 when every value is zero, else 2^k
+ * with the least k >= -126 for which every finite magnitude is at most 448 * 2^k.  With
+ * powers of two the division x / scale is exact, so a code is x rounded once (to
+ * nearest, ties to even), and raising a page's scale when later tokens need it only
+ * re-rounds codes that leave e4m3's normal range.  The calls that read a cache take any
+ * finite scales >= 0. */
+typedef struct hspec_kv8_view {
+  void* k_codes;               /* device [num_pages, Hkv, page_size, D] e4m3, 16-byte aligned */
+  void* v_codes;               /* device, the same shape                                  */
+  float* k_scales;             /* device [num_pages, Hkv]                                 */
+  float* v_scales;             /* device [num_pages, Hkv]                                 */
+  int num_pages;               /* pages in the pools                                      */
+  const int32_t* page_table;   /* device [C, max_pages], as in hspec_kv_view              */
+  int max_pages;               /* page-table width                                        */
+} hspec_kv8_view;
+
+/* Quantises new tokens into the cache.  Row cu_new[c] + i of k_new / v_new is token
+ * first[c] + i of request c, i < cu_new[c+1] - cu_new[c] (ragged; 0 new tokens are fine).
+ * A page that the range enters at slot 0 starts afresh; one that it enters later holds
+ * tokens already (slots before the range): its scale becomes max(old, that of the new
+ * values) and the earlier codes are rewritten as e4m3(code * (old / new)) when it rose.
+ * Slots past the range keep their bytes.  NaN is stored as NaN; an infinity is left out
+ * of the scale's choice and stored as +-448 * scale.
+ * k_new, v_new device [T, Hkv, D] (cfg->dtype), rows row_stride elements apart (0 = Hkv*D,
+ *   else >= Hkv*D: the k and v columns of a fused projection's output can be given as is);
+ * cu_new device [C+1] int32, 0 <= cu_new[0] <= ... <= cu_new[C] <= T (rows outside
+ *   [cu_new[0], cu_new[C]) are not read);  first device [C] int32, tokens already cached.
+ * A page may be written by one request's range only (pages that several requests share
+ * must lie before every writer's first page); two ranges on one page leave codes of both
+ * under one of their scales.  A bad cu_new pair, a range past max_pages * page_size or a
+ * bad page id sets the device error word and writes nothing for that request or page.
+ * C >= 1, 0 <= T <= 2^30. */
+HSPEC_API hspec_status hspec_kv8_write(const hspec_cfg* cfg, const void* k_new, const void* v_new,
+                                       long long row_stride, const int32_t* cu_new, const int32_t* first, int C,
+                                       int T, const hspec_kv8_view* kv, void* stream);
+
+/* Reads tokens back: row cu[c] + i of k_out / v_out = code * scale of token first[c] + i of
+ * request c, rounded once to cfg->dtype (first NULL = 0).  Arguments as for the write;
+ * rows outside every range are left as they were, and a token whose page id is bad is
+ * written as zeros (the device error word is set). */
+HSPEC_API hspec_status hspec_kv8_read(const hspec_cfg* cfg, const hspec_kv8_view* kv, const int32_t* cu,
+                                      const int32_t* first, int C, int T, void* k_out, void* v_out,
+                                      long long row_stride, void* stream);
+
+/* Workspace bytes of hspec_attn_paged_block_kv8 for C requests of K query positions and a
+ * page table of width max_pages. */
+HSPEC_API size_t hspec_attn_kv8_workspace_size(const hspec_cfg* cfg, int C, int K, int max_pages);
+
+/* Paged in-place GQA attention over the 8-bit cache, scale 1/sqrt(D), in two forms:
+ *  - k_blk, v_blk given (a draft block): query (c, j, h) sees the ctx_lens[c] cached
+ *    tokens, then the block's keys (i <= j only with HSPEC_FLAG_CAUSAL_BLOCK), as
+ *    hspec_attn_paged_block does over a bf16 cache;
+ *  - k_blk = v_blk = NULL (decoding, or verifying K tokens that are in the cache
+ *    already): query j sees all ctx_lens[c] cached tokens, or with
+ *    HSPEC_FLAG_CAUSAL_BLOCK those before position ctx_lens[c] - (K - 1) + j.  A query
+ *    that sees none gives zeros.
+ * Cached values enter as the exact code * scale of their page.  On the tensor-core path
+ * (bf16, D = 64 or 128, page_size a multiple of 16) the softmax weights enter the
+ * product with V as two e4m3 parts, at least 8 significant bits for weights from 1 down
+ * to 2^-12 of a row's largest -- fewer below, and in pages whose V scale is far smaller
+ * than the largest one of the request and head (a page 2^-13 of it keeps 8 bits, each
+ * further factor of two takes one) -- and non-finite query, block key or block value
+ * elements enter as NaN.  A NaN in the values of one of the last K tokens makes every
+ * element of the rows that see it NaN.  Other shapes run on the CUDA cores in fp32
+ * (head_dim <= 256, any page size, any group).
+ * q, out device [C, K, Hq, D] (dtype); k_blk, v_blk device [C, K, Hkv, D] (dtype) or both
+ * NULL; ctx_lens device [C] int32; all of them and the codes 16-byte aligned; workspace
+ * device, >= hspec_attn_kv8_workspace_size() bytes, 256-byte aligned.  C >= 1,
+ * 1 <= K <= 64.  Calls on the same batch give bit-identical results. */
+HSPEC_API hspec_status hspec_attn_paged_block_kv8(const hspec_cfg* cfg, const void* q, const hspec_kv8_view* kv,
+                                                  const int32_t* ctx_lens, const void* k_blk, const void* v_blk,
+                                                  int C, int K, void* out, void* workspace, size_t ws_bytes,
+                                                  void* stream);
+
 /* ------------------------------------------------------------- draft step */
 
 typedef struct hspec_drafter hspec_drafter;
