@@ -39,6 +39,8 @@ inline size_t split_smem(int D) {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) attn_kv8_split_kernel(const AttnKv8Args a, float scale_log2) {
+  pdl_wait();  // the previous kernel on the stream is complete from here on
+  pdl_trigger();
   extern __shared__ float4 sm4[];
   float* sm = (float*)sm4;
   const int D = a.kv.D, Dp = dim_pad(D), Hkv = a.kv.Hkv, page = a.kv.page_size;
@@ -162,6 +164,8 @@ __global__ void __launch_bounds__(kThreads) attn_kv8_split_kernel(const AttnKv8A
 // W warps per row; lane t holds the dims t + 32 i, i < E.
 template <typename T, int W, int E>
 __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const AttnKv8Args a) {
+  pdl_wait();  // the previous kernel on the stream is complete from here on
+  pdl_trigger();
   constexpr int RPC = 8 / W;  // rows per CTA
   __shared__ float s_acc[W > 1 ? 8 : 1][32 * E];
   __shared__ float s_ml[8][2];
@@ -177,8 +181,29 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const AttnKv8Args a
   const int g = h / G, row = j * G + h % G;
   const int ctx = a.ctx_lens[c];
   const bool valid = live && ctx >= 0 && ctx <= (long)a.kv.max_pages * a.kv.page_size;
-  const int ns = valid ? (ctx + (a.kb ? a.K : 0) + a.split_tokens - 1) / a.split_tokens : 0;
-  const size_t base0 = ((size_t)c * Hkv + g) * a.n_splits * R + row, stride = R;
+  // The row's partials q = 0 .. ns - 1 at rows base0 + q * stride.  CUDA-core path: one per
+  // split of (c, g).  Tensor-core path: the sequence (c, rb, g) holds t_seq tiles from unit
+  // s0 of the line, which is cut into chunks of Z units; its piece in chunk k has slot
+  // c * spr + rb * Hkv + g + k.
+  int ns = 0;
+  size_t base0, stride = R;
+  if (a.tc) {
+    const int* off = a.sched + 64;
+    const int spr = Hkv * a.n_rb, Z = a.sched[2];
+    const int rb = row / a.row_block, r = rb * Hkv + g;
+    int k0 = 0;
+    if (valid) {
+      const int tw = (off[c + 1] - off[c]) / spr, t_seq = tw - kAttn8SeqUnits;
+      const int s0 = off[c] + r * tw + kAttn8SeqUnits;
+      k0 = s0 / Z;
+      ns = t_seq > 0 ? (s0 + t_seq - 1) / Z - k0 + 1 : 0;
+    }
+    stride = R < a.row_block ? R : a.row_block;
+    base0 = ((size_t)c * spr + r + k0) * stride + row % a.row_block;
+  } else {
+    ns = valid ? (ctx + (a.kb ? a.K : 0) + a.split_tokens - 1) / a.split_tokens : 0;
+    base0 = ((size_t)c * Hkv + g) * a.n_splits * R + row;
+  }
   float M = -INFINITY, L = 0.f, o[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) o[i] = 0.f;
@@ -217,8 +242,8 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const AttnKv8Args a
 template <typename T, int W>
 void launch_merge_w(const AttnKv8Args& a, long rows, cudaStream_t s) {
   const int grid = (int)((rows + 8 / W - 1) / (8 / W));
-  if (a.kv.D <= 128) attn_kv8_merge_kernel<T, W, 4><<<grid, 256, 0, s>>>(a);
-  else attn_kv8_merge_kernel<T, W, 8><<<grid, 256, 0, s>>>(a);
+  if (a.kv.D <= 128) launch_pdl(attn_kv8_merge_kernel<T, W, 4>, grid, 256, 0, s, a);
+  else launch_pdl(attn_kv8_merge_kernel<T, W, 8>, grid, 256, 0, s, a);
   note_launch();
 }
 
@@ -246,7 +271,7 @@ bool launch_split(const AttnKv8Args& a, cudaStream_t s) {
   }
   const int nrb = cdiv((long)a.K * (a.Hq / a.kv.Hkv), kRows);
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)a.kv.D);
-  attn_kv8_split_kernel<T><<<dim3(a.n_splits, a.kv.Hkv * nrb, a.C), kThreads, smem, s>>>(a, scale_log2);
+  launch_pdl(attn_kv8_split_kernel<T>, dim3(a.n_splits, a.kv.Hkv * nrb, a.C), kThreads, smem, s, a, scale_log2);
   note_launch();
   return true;
 }
@@ -275,14 +300,26 @@ bool attn_kv8_supported(int K, int G, int D, const char** why) {
   return true;
 }
 
-size_t attn_kv8_ws_bytes(int dtype, int C, int K, int G, const Kv8& kv, int split_req) {
-  (void)dtype;
+size_t attn_kv8_ws_bytes(int dtype, int C, int K, int Hq, const Kv8& kv, int split_req) {
+  if (attn_kv8_tc_shape(dtype, kv.D, kv.page_size)) {
+    AttnKv8Args a = {};
+    a.kv = kv, a.C = C, a.K = K, a.Hq = Hq;
+    return attn_kv8_tc_plan(a, split_req, nullptr);
+  }
+  const int G = Hq / kv.Hkv;
   const Split sp = split_of(C, K, G, kv, split_req);
   const size_t rows = (size_t)C * kv.Hkv * sp.n * K * G;
   return rows * (kv.D + 2) * sizeof(float);
 }
 
 bool attn_kv8(int dtype, AttnKv8Args& a, int split_req, void* ws, cudaStream_t s) {
+  a.tc = attn_kv8_tc_shape(dtype, a.kv.D, a.kv.page_size);
+  if (a.tc) {
+    attn_kv8_tc_plan(a, split_req, ws);
+    if (!attn_kv8_tc_launch(a, s)) return false;
+    launch_merge<bf16>(a, s);
+    return true;
+  }
   const int G = a.Hq / a.kv.Hkv;
   const Split sp = split_of(a.C, a.K, G, a.kv, split_req);
   if (a.C > 65535 || (long)a.kv.Hkv * cdiv((long)a.K * G, kRows) > 65535) {

@@ -1,0 +1,935 @@
+// Paged block attention over the 8-bit KV cache on the 5th-generation tensor cores (bf16
+// queries, D = 64 or 128, page_size a multiple of 16).
+//
+// Both products run on the codes as they lie in the cache (kind::f8f6f4, e4m3), with the
+// roles of keys and queries exchanged: a tile of 128 keys is the M side, the R query rows
+// of a kv head the N side,
+//     S^T [128 keys x R]  = K [128 x D] . Q^T           (K straight from the page, K-major)
+//     O^T [D x R]        += V^T [D x 128 keys] . P^T    (V straight from the page, MN-major)
+// so that a thread's TMEM lane is a key, whose page scales are one register each, and the
+// tensor time falls with R (a decoded token has R = group size).  Nothing is dequantised:
+// the K scale multiplies S^T, the V scale the weights P.
+//
+// Rounding.  A bf16 query row is scaled by a power of two and held as two e4m3 parts,
+// hi + lo, which carry its 8 bits (down to 2^-17 of the row's largest element); both are
+// multiplied with K into one fp32 accumulator.  The weights p = 2^(s - m) <= 2^3 enter as
+// P = p * 2^5 * (V scale / largest V scale so far), hi = e4m3(P) and lo = e4m3(16 (P - hi))
+// side by side in one N = 2R product, O = O_hi + O_lo / 16: at least 8 bits down to 2^-12
+// of the running maximum.  Row sums use the unrounded fp32 weights.  The block's own bf16
+// keys and values are two e4m3 parts with a power-of-two scale per row, too.
+//
+// The running maximum m of a query is reduced across the 128 lanes only when some weight
+// would exceed 2^3 (or a V scale the largest so far): each tile, a thread looks at the
+// largest exponent of its own key over all its queries and one barrier with an OR tells
+// the group; O and the sums are then rescaled.  The first tile of a piece always does it.
+//
+// Work partition: as the bf16 path's, the sequences (request, row block, kv head) lie end
+// to end on a line of units, kAttn8SeqUnits for a start and one per 128-key tile; the line
+// is cut into one chunk per SM, and a piece (one sequence's tiles in a chunk) writes one
+// partial for the merge kernel.  The preparation kernel sums the line and, in its other
+// CTAs, writes the queries' and the block's two-part images in their shared-memory layout,
+// each then one bulk copy.
+//
+// Warp roles (512 threads, one CTA per SM): warps 0..3 producers (a tile's K and V pages
+// as TMA boxes of up to 128 rows, spread over the warps, and the pages' scales); warp 4
+// issues S^T, warp 5 O^T (warp 4 owns TMEM); warps 8..11 and 12..15 are two softmax groups
+// that take one half of the query columns each, so O has one accumulator.
+// Bound by HBM: 2 D bytes a key and kv head.  Every wait gives up after a time bound and
+// sets the device error word.
+#include <stdint.h>
+
+#include "../../include/hspec.h"
+#include "common.cuh"
+#include "kernels.cuh"
+#include "kv8.cuh"
+#include "tc_prims.cuh"
+
+namespace hspec {
+namespace {
+
+constexpr int TT = kAttn8Tile;  // keys per tile
+constexpr int NPW = 4;          // producer warps
+constexpr int SM_WARP0 = 8;     // first softmax warp (a multiple of 4: warp % 4 is its TMEM quarter)
+constexpr int THREADS = 512;
+constexpr float kPScale = 32.f;   // 2^5: weights enter P times this
+constexpr float kMaxExp = 3.f;    // a weight's exponent may reach this before the maximum moves
+constexpr float kLoScale = 16.f;  // the low part of P is held times this
+constexpr int kMaxChunksAuto = 256, kMaxChunksExplicit = 2048;
+constexpr int kBlkRows = 64;      // scales of a block's rows (K <= 64)
+
+// Rows of a block's images: its K keys in whole 32-key steps of the product with V.
+__host__ __device__ inline int blk_rows(int K) { return (K + 31) & ~31; }
+
+// Byte offset of 16-byte chunk `ch` of row r in rows of D bytes swizzled over D-byte spans.
+template <int D>
+__device__ __forceinline__ uint32_t swz(int r, int ch) {
+  return (uint32_t)(r * D + ((D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) << 4));
+}
+
+// Query image of a sequence: hi rows, lo rows (NR rows of D bytes each, swizzled), then
+// the rows' scales (fp32).
+__host__ __device__ inline size_t q_img_bytes(int NR, int D) { return (size_t)NR * (2 * D + 4); }
+
+template <int D, int NR>
+struct Lay {
+  static constexpr int NC = NR / 2;                       // query columns per softmax group
+  static constexpr int PN = NR == 128 ? 256 : 128;        // columns of O^T: hi from 0, lo from PN / 2
+  static constexpr int NQ = NR == 128 ? 1 : 2;            // query buffers
+  static constexpr int Q_BYTES = NR * (2 * D + 4);
+  static constexpr int Q_BUF = (Q_BYTES + 1023) & ~1023;
+  static constexpr int KV = TT * D;                       // one operand of a stage
+  static constexpr int STAGE = 2 * KV;
+  static constexpr int P_BUF = TT * PN;                   // one byte an element
+  static constexpr int OFF_P = 0;
+  static constexpr int OFF_Q = 2 * P_BUF;
+  static constexpr int OFF_KV = OFF_Q + NQ * Q_BUF;
+  static constexpr int MISC = 6144;
+  static constexpr int ROOM = (227 * 1024 - 1024 - MISC - OFF_KV) / STAGE;
+  static constexpr int NS = ROOM < 8 ? ROOM : 8;          // K/V ring stages
+  static constexpr int OFF_MISC = OFF_KV + NS * STAGE;
+  static constexpr int SMEM = OFF_MISC + MISC + 1024;
+  static constexpr uint32_t TMEM_COLS = NR == 128 ? 512 : 256;
+  __host__ __device__ static constexpr uint32_t S_COL(int b) { return (uint32_t)(PN + b * NR); }
+  static_assert(NS >= 3, "ring");
+  static_assert(PN + 2 * NR <= (int)TMEM_COLS, "TMEM");
+};
+
+struct TileMeta {  // written by producer warp 0 before the stage's barrier arrive
+  int end;         // 1: no more work (nothing else is set)
+  int c, g, rb, slot;  // request, kv head, row block; partial slot of the piece
+  int valid;       // keys in the tile
+  int first, last; // first / last tile of its piece
+  int block;       // 1: the block's own keys
+  int joff;        // key i of the tile is seen by the positions j >= joff + i
+  int mixed;       // 1: some key of the tile is hidden from some position
+  int qslot, qpar; // query buffer of the piece and the parity of its load
+};
+
+template <int NR>
+struct Misc {
+  uint64_t kv_full[8], kv_empty[8], s_full[2], s_free[2], p_full[2], pv_done[2], q_full[2], q_empty[2], scan[2], drain[2];
+  uint32_t tmem;
+  TileMeta meta[8];
+  float scale[8][16];       // per stage: K scales of its eight 16-key groups, then V scales
+  alignas(16) float2 col[NR];  // (query row's scale, -maximum)
+  alignas(16) float alpha[NR];
+  float m[NR];
+  float cmax[2][4][NR / 2]; // per group and warp: column maxima, later the rows' sums
+  float svmax[2][4];
+};
+
+struct Maps {
+  CUtensorMap k, v;
+};
+
+__device__ __forceinline__ int seq_units(int ctx, long max_ctx, int nbt) {
+  const int tiles = ctx < 0 || ctx > max_ctx ? 0 : (ctx + TT - 1) / TT + nbt;
+  return tiles > 0 ? kAttn8SeqUnits + tiles : 0;
+}
+
+// Two e4m3 parts of four values (NaN for a value that is not finite).
+__device__ __forceinline__ void split4(const float (&x)[4], uint32_t& hi, uint32_t& lo) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = fabsf(x[i]) <= 3.402823466e38f ? x[i] : __int_as_float(0x7fffffff);
+  hi = e4m3x4(v[0], v[1], v[2], v[3]);
+  const float2 a = e4m3x2_to_f2(hi), b = e4m3x2_to_f2(hi >> 16);
+  lo = e4m3x4(v[0] - a.x, v[1] - a.y, v[2] - b.x, v[3] - b.y);
+}
+
+// Power of two that takes a row of largest magnitude m to [128, 256), and its inverse.
+__device__ __forceinline__ float row_factor(float m, float& inv) {
+  const int e = max(__float_as_int(m) >> 23, 27);  // biased exponent; 2^-100 at least
+  inv = __int_as_float((e - 7) << 23);
+  return __int_as_float((254 + 7 - e) << 23);
+}
+
+// CTA 0: the line's offsets and the partition.  The others: two-part images, one warp per
+// row: query rows first, then the blocks' K and V rows.
+template <int D>
+__global__ void __launch_bounds__(256) attn_kv8_prep_kernel(const AttnKv8Args a, int grid) {
+  pdl_wait();  // the previous kernel on the stream is complete from here on
+  pdl_trigger();
+  const int Hkv = a.kv.Hkv, G = a.Hq / Hkv, R = a.K * G, NR = a.row_block;
+  if (blockIdx.x == 0) {
+    __shared__ int part[256];
+    const long max_ctx = (long)a.kv.max_pages * a.kv.page_size;
+    const int nbt = a.kb ? 1 : 0, spr = Hkv * a.n_rb;
+    int* off = a.sched + 64;
+    const int per = (a.C + 255) / 256;
+    const int c0 = min(a.C, (int)threadIdx.x * per), c1 = min(a.C, c0 + per);
+    int sum = 0;
+    for (int c = c0; c < c1; ++c) {
+      const int ctx = a.ctx_lens[c];
+      if (ctx < 0 || ctx > max_ctx) flag_error(a.err, kErrCtxOOB);
+      sum += seq_units(ctx, max_ctx, nbt) * spr;
+    }
+    part[threadIdx.x] = sum;
+    __syncthreads();
+    for (int o = 1; o < 256; o <<= 1) {  // inclusive scan of the per-thread sums
+      const int v = threadIdx.x >= (unsigned)o ? part[threadIdx.x - o] : 0;
+      __syncthreads();
+      part[threadIdx.x] += v;
+      __syncthreads();
+    }
+    int run = threadIdx.x > 0 ? part[threadIdx.x - 1] : 0;
+    for (int c = c0; c < c1; ++c) {
+      off[c] = run;
+      run += seq_units(a.ctx_lens[c], max_ctx, nbt) * spr;
+    }
+    if (threadIdx.x == 255) {
+      const int T = part[255];
+      int Z = a.chunk_units > 0 ? a.chunk_units : (T + grid - 1) / grid;
+      Z = max(max(Z, (T + a.max_chunks - 1) / a.max_chunks), 1);
+      off[a.C] = T;
+      a.sched[1] = T;
+      a.sched[2] = Z;
+      a.sched[3] = (T + Z - 1) / Z;
+    }
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const long w = (long)(blockIdx.x - 1) * 8 + (threadIdx.x >> 5);
+  const long q_rows = (long)a.C * Hkv * a.n_rb * NR;
+  const int KP = blk_rows(a.K);
+  const long b_rows = a.kb ? (long)a.C * Hkv * 2 * KP : 0;
+  if (w >= q_rows + b_rows) return;
+  // four elements per lane (D = 64: half the lanes)
+  const bool on = lane * 4 < D;
+  const bf16* src = nullptr;
+  uint8_t* hi;
+  size_t lo_off;
+  float* scale;
+  int r;
+  if (w < q_rows) {
+    r = (int)(w % NR);
+    const long seq = w / NR;  // (c * n_rb + rb) * Hkv + g
+    const int g = (int)(seq % Hkv), rb = (int)(seq / Hkv % a.n_rb), c = (int)(seq / Hkv / a.n_rb);
+    const int row = rb * NR + r;
+    if (row < R) src = (const bf16*)a.q + (size_t)(c * a.K + row / G) * a.q_rs + (size_t)(g * G + row % G) * D;
+    hi = a.q_img + seq * q_img_bytes(NR, D);
+    lo_off = (size_t)NR * D;
+    scale = (float*)(hi + 2 * lo_off) + r;
+  } else {
+    const long b = w - q_rows;
+    r = (int)(b % KP);
+    const int is_v = (int)(b / KP % 2);
+    const long cg = b / KP / 2;
+    const int g = (int)(cg % Hkv);
+    const long c = cg / Hkv;
+    if (r < a.K)
+      src = (const bf16*)(is_v ? a.vb : a.kb) + (size_t)(c * a.K + r) * (is_v ? a.vb_rs : a.kb_rs) + (size_t)g * D;
+    hi = a.blk_img + (cg * 4 + 2 * is_v) * (size_t)KP * D;
+    lo_off = (size_t)KP * D;
+    scale = a.blk_scale + (cg * 2 + is_v) * kBlkRows + r;
+  }
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  if (src && on) {
+    const uint2 v = *(const uint2*)(src + lane * 4);
+    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  }
+  const float m = warp_max(fmaxf(fmaxf(kv8_mag(x[0]), kv8_mag(x[1])), fmaxf(kv8_mag(x[2]), kv8_mag(x[3]))));
+  float inv;
+  const float f = row_factor(m, inv);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] *= f;
+  uint32_t h, l;
+  split4(x, h, l);
+  if (on) {
+    const uint32_t o = swz<D>(r, lane >> 2) + (lane & 3) * 4;
+    *(uint32_t*)(hi + o) = h;
+    *(uint32_t*)(hi + lo_off + o) = l;
+  }
+  if (lane == 0) *scale = inv;
+}
+
+// Order-preserving integer of a float (NaN counts as -infinity) and back.
+__device__ __forceinline__ int float_key(float v) {
+  const int i = __float_as_int(v == v ? v : -INFINITY);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float key_float(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+
+template <int D, int NR>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_kv8_tc_kernel(const __grid_constant__ Maps maps, const AttnKv8Args a, float scale_log2, int box_rows) {
+  using L = Lay<D, NR>;
+  constexpr int NS = L::NS, NC = L::NC, PN = L::PN;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = tc::smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023) & ~1023u) - raw);
+  uint8_t* sP = smem + L::OFF_P;
+  uint8_t* sQ = smem + L::OFF_Q;
+  uint8_t* sKV = smem + L::OFF_KV;
+  static_assert(sizeof(Misc<NR>) <= L::MISC, "misc area");
+  Misc<NR>& ms = *(Misc<NR>*)(smem + L::OFF_MISC);
+  volatile TileMeta* meta = ms.meta;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int Hkv = a.kv.Hkv, G = a.Hq / Hkv, R = a.K * G;
+  const int RB = R < NR ? R : NR;  // rows of a partial
+  int* err = a.err;
+  const uint64_t lim = a.wait_ns ? (uint64_t)a.wait_ns : tc::kWaitLimitNs;  // pipeline waits
+  constexpr int QK_WARP = 4, PV_WARP = 5;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      tc::mbar_init(&ms.kv_full[s], NPW);
+      tc::mbar_init(&ms.kv_empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&ms.s_full[b], 1);
+      tc::mbar_init(&ms.s_free[b], 8);
+      tc::mbar_init(&ms.p_full[b], 8);
+      tc::mbar_init(&ms.pv_done[b], 1);
+      tc::mbar_init(&ms.q_full[b], 1);
+      tc::mbar_init(&ms.q_empty[b], 1);
+      tc::mbar_init(&ms.drain[b], 1);
+      tc::mbar_init(&ms.scan[b], 4);
+    }
+    tc::fence_mbar_init();
+  }
+  if (warp == QK_WARP) tc::tmem_alloc(&ms.tmem, L::TMEM_COLS);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = ms.tmem;
+  pdl_wait();  // the previous kernel on the stream is complete from here on
+  pdl_trigger();
+
+  if (warp < NPW) {
+    // ------------------------------------------------------------ producers
+    // Box bx < nb is rows [bx box_rows, ...) of K, box nb + bx of V, issued by lane bx / 4
+    // of warp bx % 4.  Lanes 16..19 of warp w bring the scales of the 16-key groups 2w
+    // and 2w + 1 (K, K, V, V).  All producer warps walk the same tiles; warp 0 loads the
+    // queries and describes the tile.
+    const int pw = warp, nb = TT / box_rows;
+    const int bx = pw + NPW * lane;
+    const bool has_box = lane < 16 && bx < 2 * nb;
+    const bool has_scale = lane >= 16 && lane < 20;
+    const int grp = 2 * pw + (lane & 1);
+    const bool is_v = has_scale ? (lane & 2) != 0 : bx >= nb;
+    const int sub = has_scale ? 16 * grp : (bx % nb) * box_rows;  // first key of the tile that concerns the lane
+    const float* scales = is_v ? a.kv.vs : a.kv.ks;
+    if (threadIdx.x == 0) {
+      tc::tma_prefetch_desc(&maps.k);
+      tc::tma_prefetch_desc(&maps.v);
+    }
+    const int spr = Hkv * a.n_rb;  // sequences per request
+    const int page = a.kv.page_size;
+    const int T = a.sched[1], Z = a.sched[2], n_chunks = a.sched[3];
+    const int* off = a.sched + 64;
+    // the request holding unit p of the line: the last c with off[c] <= p
+    auto locate = [&](int p) -> int {
+      int lo = 0, hi = a.C - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (off[mid] <= p) lo = mid;
+        else hi = mid - 1;
+      }
+      return lo;
+    };
+    const uint64_t once = tc::l2_evict_first();  // the cache is read once
+    int k = blockIdx.x;  // this CTA's chunk
+    int pos = k < n_chunks ? k * Z : 0, end = k < n_chunks ? min(T, pos + Z) : 0;
+    int c = pos < end ? locate(pos) : 0;
+    int tile_i = 0;   // tiles this warp has armed (its arrival on their stage)
+    int q_last = -1;  // warp 0: the last piece whose queries it armed
+    bool ok = true;
+    // Every producer warp walks the same pieces and passes the same barriers: the loop
+    // ends only at one, when the work is done or a producer has given up waiting.
+    bool stopped = false;
+    for (int seq = 0;; ++seq) {
+      if (tc::bar_or<1, 32 * NPW>(!ok)) {
+        stopped = true;
+        break;
+      }
+      int r = 0, lt0 = 0, n_tiles = 0;
+      bool done = false;
+      while (n_tiles == 0) {
+        if (pos >= end) {  // the CTA's next chunk
+          k += gridDim.x;
+          if (k >= n_chunks) {
+            done = true;
+            break;
+          }
+          pos = k * Z;
+          end = min(T, pos + Z);
+          c = locate(pos);
+        }
+        while (off[c + 1] <= pos) ++c;
+        const int tw = (off[c + 1] - off[c]) / spr;
+        const int rel = pos - off[c];
+        r = rel / tw;
+        const int u0 = rel - r * tw, u1 = min(tw, u0 + (end - pos));
+        pos += u1 - u0;
+        lt0 = max(u0 - kAttn8SeqUnits, 0);
+        n_tiles = max(u1 - kAttn8SeqUnits - lt0, 0);
+      }
+      if (done) break;
+      const int g = r % Hkv, rb = r / Hkv;
+      const int ctx = a.ctx_lens[c];
+      const int ct = (ctx + TT - 1) / TT;  // context tiles of the sequence
+      const int qslot = seq % L::NQ, quse = seq / L::NQ;
+
+      // the piece's queries into buffer `qslot` once the piece before in it is done
+      if (pw == 0) {
+        if (lane == 0) {
+          ok = tc::mbar_wait(&ms.q_empty[qslot], (quse & 1) ^ 1, err, lim);
+          if (ok) {
+            q_last = seq;
+            tc::mbar_arrive_expect_tx(&ms.q_full[qslot], (uint32_t)L::Q_BYTES);
+            tc::bulk_load(sQ + qslot * L::Q_BUF, a.q_img + ((size_t)c * spr + r) * L::Q_BYTES, (uint32_t)L::Q_BYTES,
+                          &ms.q_full[qslot]);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        q_last = __shfl_sync(0xffffffffu, q_last, 0);
+      }
+
+      // Page ids of the lane's keys two tiles ahead and scales one tile ahead, in
+      // registers (the table index clamped into the request's row: ids past the context's
+      // end are never used).
+      const int32_t* table = a.kv.table + (size_t)c * a.kv.max_pages;
+      auto page_of = [&](int local) -> int {
+        const int idx = ((lt0 + local) * TT + sub) / page;
+        return table[idx < a.kv.max_pages ? idx : a.kv.max_pages - 1];
+      };
+      auto scale_of = [&](int pid) -> float {
+        return has_scale && pid >= 0 && pid < a.kv.num_pages ? scales[(size_t)pid * Hkv + g] : 0.f;
+      };
+      int pid0 = page_of(0), pid1 = page_of(1);
+      float sc0 = scale_of(pid0);
+
+      for (int local = 0; local < n_tiles && ok; ++local, ++tile_i) {
+        const int pid = pid0;
+        const float sc = sc0;
+        pid0 = pid1;
+        sc0 = scale_of(pid0);
+        pid1 = page_of(local + 2);
+        const int s = tile_i % NS;
+        ok = tc::mbar_wait_warp(&ms.kv_empty[s], ((tile_i / NS) & 1) ^ 1, err, lim);
+        if (!ok) break;
+        uint8_t* kd = sKV + s * L::STAGE;
+        uint8_t* vd = kd + L::KV;
+        const int st = lt0 + local;  // tile of the sequence
+        const bool block = st >= ct;
+        const int t0 = st * TT;
+        const int valid = block ? a.K : min(TT, ctx - t0);
+        if (has_scale) ms.scale[s][(is_v ? 8 : 0) + grp] = sc;
+        if (pw == 0 && lane == 0) {
+          volatile TileMeta& m = meta[s];
+          const int joff = !a.causal ? -TT : block ? 0 : a.kb ? -TT : max(t0 - ctx + a.K, -TT);
+          m.end = 0, m.c = c, m.g = g, m.rb = rb, m.slot = c * spr + r + k, m.valid = valid;
+          m.first = local == 0, m.last = local == n_tiles - 1, m.block = block;
+          m.joff = joff, m.mixed = joff + valid - 1 > 0;
+          m.qslot = qslot, m.qpar = quse & 1;
+        }
+        if (block) {
+          // the block's K (warp 0) and V (warp 1) images: hi rows, then lo rows
+          const uint32_t bytes = (uint32_t)(2 * blk_rows(a.K) * D);
+          if (lane == 0) {
+            if (pw < 2) {
+              tc::mbar_arrive_expect_tx(&ms.kv_full[s], bytes);
+              tc::bulk_load(pw == 0 ? kd : vd, a.blk_img + ((size_t)(c * Hkv + g) * 2 + pw) * bytes, bytes,
+                            &ms.kv_full[s]);
+            } else {
+              tc::mbar_arrive(&ms.kv_full[s]);
+            }
+          }
+        } else {
+          const bool mine = has_box && sub < valid;
+          const uint32_t warp_bytes = __reduce_add_sync(0xffffffffu, mine ? (uint32_t)(box_rows * D) : 0u);
+          if (lane == 0) tc::mbar_arrive_expect_tx(&ms.kv_full[s], warp_bytes);  // also this warp's arrival
+          __syncwarp();
+          if (mine) {
+            int pg = pid;
+            if (pg < 0 || pg >= a.kv.num_pages) {
+              flag_error(err, kErrPageOOB);
+              pg = 0;  // keep the copy in bounds (its scales are 0 here)
+            }
+            tc::tma_load_3d_hint((is_v ? vd : kd) + sub * D, is_v ? &maps.v : &maps.k, &ms.kv_full[s], 0,
+                                 (t0 + sub) % page, pg * Hkv + g, once);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // No copy may land after the CTA has finished: wait, with the full limit, for the last
+    // filling of every stage this warp armed, and warp 0 for its last query loads.  Before
+    // the sentinel below, which completes the next phase of one of these stages.
+    if (lane == 0) {
+      for (int j = tile_i > NS ? tile_i - NS : 0; j < tile_i; ++j)
+        tc::mbar_wait(&ms.kv_full[j % NS], (j / NS) & 1, err);
+      for (int q = max(q_last - L::NQ + 1, 0); q <= q_last; ++q)
+        tc::mbar_wait(&ms.q_full[q % L::NQ], (q / L::NQ) & 1, err);
+    }
+    __syncwarp();
+    // sentinel stage: no more work
+    if (!stopped) {
+      const int s = tile_i % NS;
+      if (tc::mbar_wait_warp(&ms.kv_empty[s], ((tile_i / NS) & 1) ^ 1, err, lim) && lane == 0) {
+        if (pw == 0) meta[s].end = 1;
+        tc::mbar_arrive(&ms.kv_full[s]);
+      }
+    }
+  } else if (warp == QK_WARP) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- S^T issuer
+      // S^T_b = K_i . Q^T into S buffer b = i % 2 once tile i has landed, the softmax has
+      // read tile i - 2 out of S_b and the piece's queries are there.
+      constexpr uint32_t idesc = tc::idesc_e4m3_f32(TT, NR, false, false);
+      for (int i = 0;; ++i) {
+        const int s = i % NS, b = i & 1;
+        if (!tc::mbar_wait(&ms.kv_full[s], (i / NS) & 1, err, lim)) break;
+        if (meta[s].end) break;
+        if (meta[s].first && !tc::mbar_wait(&ms.q_full[meta[s].qslot], meta[s].qpar, err, lim)) break;
+        if (i >= 2 && !tc::mbar_wait(&ms.s_free[b], ((i >> 1) - 1) & 1, err, lim)) break;
+        tc::tc_fence_after();
+        const uint32_t q = tc::smem_u32(sQ + meta[s].qslot * L::Q_BUF), kt = tc::smem_u32(sKV + s * L::STAGE);
+        // block tiles: the low parts of K follow its high parts
+        const int parts = meta[s].block ? 2 : 1;
+        for (int p = 0; p < parts; ++p) {
+          const uint32_t kp = kt + p * blk_rows(a.K) * D;
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) {
+            tc::mma_e4m3(tmem + L::S_COL(b), tc::sdesc_b8<D>(kp + kk * 32), tc::sdesc_b8<D>(q + kk * 32), idesc,
+                         (p > 0 || kk > 0) ? 1u : 0u);
+            tc::mma_e4m3(tmem + L::S_COL(b), tc::sdesc_b8<D>(kp + kk * 32), tc::sdesc_b8<D>(q + NR * D + kk * 32),
+                         idesc, 1u);
+          }
+        }
+        tc::mma_commit(&ms.s_full[b]);
+      }
+      // no MMA or commit arrival may land after the CTA has finished
+      tc::mma_commit(&ms.drain[0]);
+      tc::mbar_wait(&ms.drain[0], 0, err);
+    }
+  } else if (warp == PV_WARP) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- O^T issuer
+      // O^T += V_i^T . P_i^T in steps of 32 keys (V rows past the last key are zero) once
+      // P_i is in shared memory; its commit frees the K/V stage (S^T_i finished before
+      // that tile's softmax began) and the P buffer.
+      constexpr uint32_t idesc = tc::idesc_e4m3_f32(D, PN, true, true);
+      for (int i = 0;; ++i) {
+        const int s = i % NS, b = i & 1;
+        if (!tc::mbar_wait(&ms.kv_full[s], (i / NS) & 1, err, lim)) break;
+        if (meta[s].end) break;
+        if (!tc::mbar_wait(&ms.p_full[b], (i >> 1) & 1, err, lim)) break;
+        tc::tc_fence_after();
+        const uint32_t p = tc::smem_u32(sP + b * L::P_BUF), vt = tc::smem_u32(sKV + s * L::STAGE + L::KV);
+        const int steps = (meta[s].valid + 31) / 32, parts = meta[s].block ? 2 : 1;
+        for (int h = 0; h < parts; ++h) {
+          const uint32_t vp = vt + h * blk_rows(a.K) * D;
+          for (int kk = 0; kk < steps; ++kk)
+            tc::mma_e4m3(tmem, tc::sdesc_b8<D>(vp + kk * 32 * D), tc::sdesc_b8<128>(p + kk * 32 * 128, TT * 128), idesc,
+                         (h > 0 || kk > 0 || !meta[s].first) ? 1u : 0u);
+        }
+        if (meta[s].last) tc::mbar_arrive(&ms.q_empty[meta[s].qslot]);
+        tc::mma_commit(&ms.kv_empty[s]);
+        tc::mma_commit(&ms.pv_done[b]);
+      }
+      tc::mma_commit(&ms.drain[1]);
+      tc::mbar_wait(&ms.drain[1], 0, err);
+    }
+  } else if (warp >= SM_WARP0) {
+    // ------------------------------------------------------------ softmax groups
+    // Group w holds the query columns [w NC, (w + 1) NC); the thread's key is its lane of
+    // the tile.  A wait that gave up (ok = false) is acted on only at the group's barriers,
+    // so that all four warps leave together.
+    const int w = (warp - SM_WARP0) >> 2, quarter = warp & 3;
+    const int key = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t t_hi = tmem + lane_off + w * NC, t_lo = t_hi + PN / 2;
+    auto group_or = [&](bool p) -> bool {
+      return w == 0 ? tc::bar_or<2, 128>(p) : tc::bar_or<3, 128>(p);
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, err, lim));
+    };
+    float l[NC];        // this key lane's share of the columns' sums
+    float Mv = 0.f, inv_mv = 0.f;  // largest V scale of the piece, 1 / it
+    bool ok = true;
+    uint32_t scans = 0;  // bit b: parity of the scans of tiles i = b (mod 2)
+    // the previous piece's partial, still in O^T
+    bool pend = false;
+    size_t pend_base = 0;
+    int pend_rows = 0, pend_i = 0;
+    float pend_mul = 0.f;
+    // O^T after the product of tile i, times mul, to rows base.. of the workspace
+    auto write_partial = [&](int i, size_t base, int rows, float mul) -> bool {
+      if (!wait(&ms.pv_done[i & 1], (i >> 1) & 1)) return false;
+      tc::tc_fence_after();
+      const int d = D == 128 ? key : quarter * 16 + lane;
+      const bool on = D == 128 || lane < 16;
+      constexpr int CH = NC < 16 ? NC : 16;
+#pragma unroll
+      for (int j0 = 0; j0 < NC; j0 += CH) {
+        float hi[CH], lo[CH];
+        tc::tmem_ld(t_hi + j0, hi);
+        tc::tmem_ld(t_lo + j0, lo);
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+          if (on && w * NC + j0 + j < rows)
+            a.ws_acc[(base + w * NC + j0 + j) * D + d] = fmaf(lo[j], 1.f / kLoScale, hi[j]) * mul;
+      }
+      return true;
+    };
+
+    for (int i = 0;; ++i) {
+      const int s = i % NS, b = i & 1;
+      bool end = false;
+      if (ok) {
+        ok = wait(&ms.kv_full[s], (i / NS) & 1);
+        end = ok && meta[s].end != 0;
+        if (ok && !end) ok = wait(&ms.s_full[b], (i >> 1) & 1);
+      }
+      const bool run = ok && !end;
+      bool first = false, last = false, mixed = false, block = false;
+      int valid = 0, cmin = 0, rb = 0, slot = 0;
+      const float* cq_first = nullptr;
+      float e[NC], sv = 0.f;
+      float e_max = -INFINITY;
+      if (run) {
+        first = meta[s].first != 0, mixed = meta[s].mixed != 0, block = meta[s].block != 0;
+        last = meta[s].last != 0, valid = meta[s].valid, rb = meta[s].rb, slot = meta[s].slot;
+        tc::tc_fence_after();
+        tc::tmem_ld(tmem + lane_off + L::S_COL(b) + w * NC, e);
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ms.s_free[b]);
+        float ck = 0.f;
+        if (block) {
+          const float* bs = a.blk_scale + (size_t)(meta[s].c * Hkv + meta[s].g) * 2 * kBlkRows;
+          if (key < valid) ck = bs[key], sv = bs[kBlkRows + key];
+        } else if (key < valid) {
+          ck = ms.scale[s][key >> 4], sv = ms.scale[s][8 + (key >> 4)];
+        }
+        ck *= scale_log2;
+        // columns below cmin do not see this key (row = rb NR + column, position row / G)
+        cmin = key >= valid ? NR : max(meta[s].joff + key, 0) * G - rb * NR;
+        if (first) {
+          ok = wait(&ms.q_full[meta[s].qslot], meta[s].qpar);
+          cq_first = (const float*)(sQ + meta[s].qslot * L::Q_BUF + 2 * NR * D) + w * NC;
+        }
+        const float2 ck2 = make_float2(ck, ck);
+#pragma unroll
+        for (int j = 0; j < NC; j += 2) {
+          const float2 u = tc::fmul2(make_float2(e[j], e[j + 1]), ck2);
+          if (first) {
+            e[j] = u.x * cq_first[j], e[j + 1] = u.y * cq_first[j + 1];
+          } else {
+            const float4 cm = *(const float4*)&ms.col[w * NC + j];
+            const float2 x = tc::ffma2(u, make_float2(cm.x, cm.z), make_float2(cm.y, cm.w));
+            e[j] = x.x, e[j + 1] = x.y;
+          }
+        }
+        if (cmin > w * NC) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+            if (w * NC + j < cmin) e[j] = -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < NC; ++j) e_max = fmaxf(e_max, e[j]);
+      }
+      if (group_or(!run || !ok || first || e_max > kMaxExp || sv > Mv)) {
+        // The maxima move (or the group leaves).  s = e + m (e alone in a first tile).
+        if (run) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j) {
+            const float v = first ? e[j] : e[j] - ms.col[w * NC + j].y;
+            e[j] = v;
+            const int top = __reduce_max_sync(0xffffffffu, float_key(v));
+            if (lane == (j & 31)) ms.cmax[w][quarter][j] = key_float(top);
+          }
+          const float t = warp_max(sv);
+          if (lane == 0) ms.svmax[w][quarter] = t;
+        }
+        if (group_or(!run || !ok)) break;
+        if (quarter == 0) {
+          for (int j = lane; j < NC; j += 32) {
+            const float cm = fmaxf(fmaxf(ms.cmax[w][0][j], ms.cmax[w][1][j]), fmaxf(ms.cmax[w][2][j], ms.cmax[w][3][j]));
+            const int col = w * NC + j;
+            const float m_old = first ? -INFINITY : ms.m[col], m_new = fmaxf(m_old, cm);
+            const float cq = first ? cq_first[j] : ms.col[col].x;
+            ms.m[col] = m_new;
+            ms.col[col] = make_float2(cq, m_new == -INFINITY ? 0.f : -m_new);
+            ms.alpha[col] = m_old == -INFINITY ? 1.f : exp2f(m_old - m_new);
+          }
+        }
+        const float sv_top = fmaxf(fmaxf(ms.svmax[w][0], ms.svmax[w][1]), fmaxf(ms.svmax[w][2], ms.svmax[w][3]));
+        const float mv_new = first ? sv_top : fmaxf(Mv, sv_top);
+        const float mv_ratio = mv_new > 0.f ? Mv / mv_new : 0.f;
+        Mv = mv_new;
+        inv_mv = Mv > 0.f ? fminf(1.f / Mv, 3.402823466e38f) : 0.f;
+        group_or(false);  // col, m and alpha are written
+        if (first) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j) l[j] = 0.f;
+        } else {
+#pragma unroll
+          for (int j = 0; j < NC; ++j) l[j] *= ms.alpha[w * NC + j];
+          // O^T holds the piece's earlier tiles once the product of tile i - 1 is done
+          ok = wait(&ms.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
+          if (ok) {
+            tc::tc_fence_after();
+            constexpr int CH = 8;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j0 = 0; j0 < NC; j0 += CH) {
+                float o[CH];
+                const uint32_t t = (h ? t_lo : t_hi) + j0;
+                tc::tmem_ld(t, o);
+#pragma unroll
+                for (int j = 0; j < CH; ++j) o[j] *= ms.alpha[w * NC + j0 + j] * mv_ratio;
+                tc::tmem_st8(t, o);
+              }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NC; ++j) e[j] += ms.col[w * NC + j].y;
+      }
+      // From here on a failed wait only skips work; the group leaves at the next barrier.
+      const float rv = sv * inv_mv * kPScale;
+      uint32_t hi[NC / 4], lo[NC / 4];
+#pragma unroll
+      for (int j = 0; j < NC; j += 4) {
+        uint32_t hh[2], ll[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 p = make_float2(tc::ex2_ftz(e[j + 2 * k]), tc::ex2_ftz(e[j + 2 * k + 1]));
+          const float2 ls = tc::fadd2(make_float2(l[j + 2 * k], l[j + 2 * k + 1]), p);
+          l[j + 2 * k] = ls.x, l[j + 2 * k + 1] = ls.y;
+          const float2 pv = tc::fmul2(p, make_float2(rv, rv));
+          // fp16 first (11 bits, well below the two parts' error): the parts' differences
+          // are then packed half arithmetic
+          const __half2 ph = __floats2half2_rn(pv.x, pv.y);
+          hh[k] = e4m3x2_h(ph);
+          const __half2 d = __hfma2(ph, __float2half2_rn(kLoScale), __hmul2(e4m3x2_to_h2(hh[k]), __float2half2_rn(-kLoScale)));
+          ll[k] = e4m3x2_h(d);
+        }
+        hi[j / 4] = hh[0] | (hh[1] << 16);
+        lo[j / 4] = ll[0] | (ll[1] << 16);
+      }
+      // The P buffer is free once the product of tile i - 2 is done.  (Before the scan: a
+      // group's scan of tile i + 2 then follows both groups' scans of tile i, and the
+      // phases of a scan barrier stay at most one ahead of its waiter.)
+      if (ok && i >= 2) ok = wait(&ms.pv_done[b], ((i >> 1) - 1) & 1);
+      // a NaN in a V row that some column does not see: the product would carry it into
+      // that column, too, so the row is cleared and the columns that see it get a NaN sum
+      bool bad = false;
+      uint8_t* v_row = sKV + s * L::STAGE + L::KV + key * D;
+      if (ok && mixed) {
+        if (key < valid) {
+          const int n16 = D / 16;
+          for (int h = 0; h < (block ? 2 : 1); ++h)
+            for (int q = 0; q < n16; ++q) {
+              const uint4 x = *(const uint4*)(v_row + h * blk_rows(a.K) * D + q * 16);
+              const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int z = 0; z < 4; ++z) bad = bad || __vcmpeq4(xs[z] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+            }
+        }
+        if (w == 1) {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&ms.scan[b]);
+        } else {
+          ok = wait(&ms.scan[b], (scans >> b) & 1);  // the other group has read the rows
+          if (ok && bad)
+            for (int h = 0; h < (block ? 2 : 1); ++h)
+              for (int q = 0; q < D / 16; ++q)
+                *(uint4*)(v_row + h * blk_rows(a.K) * D + q * 16) = make_uint4(0, 0, 0, 0);
+        }
+        scans ^= 1u << b;
+        if (bad)
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+            if (w * NC + j >= cmin) l[j] = __int_as_float(0x7fffffff);
+      }
+      // V rows past the last key may hold anything (their weights are 0): clear them
+      if (ok && !block && key >= valid && key < ((valid + 31) & ~31)) {
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) *(uint4*)(v_row + w * (D / 2) + q * 16) = make_uint4(0, 0, 0, 0);
+      }
+      if (ok) {
+        uint8_t* prow = sP + b * L::P_BUF + key * 128;
+        auto put = [&](const uint32_t (&x)[NC / 4], uint8_t* base, int byte0) {
+          if constexpr (NC >= 16) {
+#pragma unroll
+            for (int q = 0; q < NC / 16; ++q)
+              *(uint4*)(base + (((byte0 / 16 + q) ^ (key & 7)) << 4)) =
+                  make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+          } else {
+            *(uint2*)(base + (((byte0 / 16) ^ (key & 7)) << 4) + (byte0 & 15)) = make_uint2(x[0], x[1]);
+          }
+        };
+        put(hi, prow, w * NC);
+        if constexpr (NR == 128) put(lo, prow + TT * 128, w * NC);
+        else put(lo, prow, 64 + w * NC);
+      }
+      tc::fence_proxy_async();
+      // the previous piece's partial, before this tile's product may overwrite O^T
+      if (ok && pend) ok = write_partial(pend_i, pend_base, pend_rows, pend_mul);
+      pend = false;
+      tc::tc_fence_before();
+      __syncwarp();
+      if (ok && lane == 0) tc::mbar_arrive(&ms.p_full[b]);
+
+      if (last) {
+        // the piece is complete: its sums now, its O^T during the next tile
+        const int rows = min(RB, R - rb * NR);
+        const size_t base = (size_t)slot * RB;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          const float t = warp_sum(l[j]);
+          if (lane == (j & 31)) ms.cmax[w][quarter][j] = t;
+        }
+        group_or(false);
+        if (quarter == 0) {
+          for (int j = lane; j < NC; j += 32)
+            if (w * NC + j < rows) {
+              float* ml = a.ws_ml + (base + w * NC + j) * 2;
+              ml[0] = ms.m[w * NC + j];
+              ml[1] = (ms.cmax[w][0][j] + ms.cmax[w][1][j]) + (ms.cmax[w][2][j] + ms.cmax[w][3][j]);
+            }
+        }
+        group_or(false);  // cmax and m may be written again
+        pend = true, pend_i = i, pend_base = base, pend_rows = rows;
+        pend_mul = Mv * (1.f / kPScale);
+      }
+    }
+    if (ok && pend) write_partial(pend_i, pend_base, pend_rows, pend_mul);
+    tc::tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == QK_WARP) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, L::TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return (EncodeTiledFn)p;
+  }();
+  return fn;
+}
+
+// Codes [num_pages * Hkv][page_size][D] bytes, box of box_rows rows of one page and head,
+// swizzled over D bytes.
+bool make_map(CUtensorMap* m, const Kv8& kv, const uint8_t* base, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)kv.D, (cuuint64_t)kv.page_size, (cuuint64_t)kv.num_pages * kv.Hkv};
+  cuuint64_t strides[2] = {(cuuint64_t)kv.D, (cuuint64_t)kv.D * kv.page_size};
+  cuuint32_t box[3] = {(cuuint32_t)kv.D, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, kv.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NR>
+bool launch(const AttnKv8Args& a, int grid, cudaStream_t s) {
+  using L = Lay<D, NR>;
+  if (cudaFuncSetAttribute(attn_kv8_tc_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) !=
+      cudaSuccess) {
+    set_error("cudaFuncSetAttribute(attn_kv8_tc_kernel) failed");
+    return false;
+  }
+  int box_rows = 16;
+  while (box_rows < TT && a.kv.page_size % (2 * box_rows) == 0) box_rows *= 2;
+  Maps maps;
+  if (!make_map(&maps.k, a.kv, a.kv.k, box_rows) || !make_map(&maps.v, a.kv, a.kv.v, box_rows)) {
+    set_error("cuTensorMapEncodeTiled failed for the 8-bit cache");
+    return false;
+  }
+  const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
+  launch_pdl(attn_kv8_tc_kernel<D, NR>, grid, THREADS, L::SMEM, s, maps, a, scale_log2, box_rows);
+  note_launch();
+  return true;
+}
+
+template <int D>
+bool launch_d(const AttnKv8Args& a, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int grid = min(sms > 0 ? sms : 148, kMaxChunksAuto);
+  const long rows = (long)a.C * a.kv.Hkv * a.n_rb * a.row_block + (a.kb ? (long)a.C * a.kv.Hkv * 2 * blk_rows(a.K) : 0);
+  launch_pdl(attn_kv8_prep_kernel<D>, 1 + (unsigned)((rows + 7) / 8), 256, 0, s, a, grid);
+  note_launch();
+  switch (a.row_block) {
+    case 16: return launch<D, 16>(a, grid, s);
+    case 32: return launch<D, 32>(a, grid, s);
+    case 64: return launch<D, 64>(a, grid, s);
+    default: return launch<D, 128>(a, grid, s);
+  }
+}
+
+}  // namespace
+
+// The pages must hold whole 16-key groups (one TMA box and one scale each); the rows are
+// one swizzle width.
+bool attn_kv8_tc_shape(int dtype, int D, int page_size) {
+  return dtype == HSPEC_DTYPE_BF16 && (D == 64 || D == 128) && page_size % 16 == 0;
+}
+
+size_t attn_kv8_tc_plan(AttnKv8Args& a, int split_req, void* ws) {
+  const int D = a.kv.D, Hkv = a.kv.Hkv, R = a.K * (a.Hq / Hkv);
+  // the narrowest N that holds the rows: the tensor time, the exponentials and the
+  // barrier work of a tile all go by it
+  a.row_block = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
+  a.n_rb = cdiv(R, a.row_block);
+  a.chunk_units = split_req > 0 ? cdiv(split_req, TT) : 0;
+  a.max_chunks = a.chunk_units > 0 ? kMaxChunksExplicit : kMaxChunksAuto;
+  const size_t seqs = (size_t)a.C * Hkv * a.n_rb;
+  const size_t rows = (seqs + a.max_chunks) * (R < a.row_block ? R : a.row_block);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* p = (uint8_t*)ws + off;
+    off += (bytes + 255) & ~(size_t)255;
+    return p;
+  };
+  uint8_t* acc = take(rows * D * 4);
+  uint8_t* ml = take(rows * 8);
+  uint8_t* sched = take((64 + (size_t)a.C + 1) * 4);
+  uint8_t* qi = take(seqs * q_img_bytes(a.row_block, D));
+  uint8_t* bi = take((size_t)a.C * Hkv * 4 * blk_rows(a.K) * D);
+  uint8_t* bs = take((size_t)a.C * Hkv * 2 * kBlkRows * 4);
+  if (ws) {
+    a.ws_acc = (float*)acc, a.ws_ml = (float*)ml, a.sched = (int*)sched;
+    a.q_img = qi, a.blk_img = bi, a.blk_scale = (float*)bs;
+  }
+  return off;
+}
+
+bool attn_kv8_tc_launch(const AttnKv8Args& a, cudaStream_t s) {
+  // the line is indexed in 32 bits
+  const long tiles = ((long)a.kv.max_pages * a.kv.page_size + TT - 1) / TT + 1;
+  if ((double)a.C * a.kv.Hkv * a.n_rb * (tiles + kAttn8SeqUnits) >= (double)(1 << 30)) {
+    set_error("attention over the 8-bit cache: too many context tiles in one call");
+    return false;
+  }
+  if ((double)a.kv.num_pages * a.kv.Hkv > 2147483647.0) {
+    set_error("attention over the 8-bit cache: pool too large");
+    return false;
+  }
+  return a.kv.D == 128 ? launch_d<128>(a, s) : launch_d<64>(a, s);
+}
+
+}  // namespace hspec

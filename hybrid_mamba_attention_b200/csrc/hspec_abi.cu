@@ -637,8 +637,7 @@ size_t hspec_attn_kv8_workspace_size(const hspec_cfg* cfg, int C, int K, int max
   if ((long)max_pages * cfg->page_size > (1L << 30)) return 0;
   hspec_kv8_view kv = {};
   kv.max_pages = max_pages;
-  return align256(attn_kv8_ws_bytes(cfg->dtype, C, K, cfg->n_q_heads / cfg->n_kv_heads, kv8_of(cfg, &kv),
-                                    cfg->attn_split_tokens));
+  return align256(attn_kv8_ws_bytes(cfg->dtype, C, K, cfg->n_q_heads, kv8_of(cfg, &kv), cfg->attn_split_tokens));
 }
 
 hspec_status hspec_attn_paged_block_kv8(const hspec_cfg* cfg, const void* q, const hspec_kv8_view* kv,

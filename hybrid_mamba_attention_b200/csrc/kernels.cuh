@@ -208,11 +208,28 @@ struct AttnKv8Args {
   bool causal;
   int split_tokens, n_splits;  // CUDA-core path: tokens per split, splits per sequence (upper bound)
   float* ws_acc; float* ws_ml; // partials
+  // tensor-core path (attn_kv8_tc.cu); the query rows of a kv head in n_rb blocks of
+  // row_block rows
+  bool tc;
+  int row_block, n_rb;
+  int max_chunks, chunk_units; // bound of the partition's chunks; requested chunk length (0: one per SM)
+  int* sched;                  // [1] units T, [2] chunk length Z, [3] chunks; from [64] the requests' offsets
+  uint8_t* q_img;              // query images, one per sequence
+  uint8_t* blk_img;            // block key / value images, one per (request, kv head)
+  float* blk_scale;            // their rows' scales [C, Hkv, 2, 64]
   int* err;
   unsigned long long wait_ns;  // pipeline waits give up after this long (0: the default)
 };
+// Tensor-core path: keys per tile, and the units that a sequence's start counts on the
+// partition's line (one unit per tile besides).
+constexpr int kAttn8Tile = 128;
+constexpr int kAttn8SeqUnits = 4;
+bool attn_kv8_tc_shape(int dtype, int D, int page_size);
+// Workspace bytes; sets the plan's fields of `a` (and with ws != NULL its pointers).
+size_t attn_kv8_tc_plan(AttnKv8Args& a, int split_req, void* ws);
+bool attn_kv8_tc_launch(const AttnKv8Args& a, cudaStream_t s);
 bool attn_kv8_supported(int K, int G, int D, const char** why);
-size_t attn_kv8_ws_bytes(int dtype, int C, int K, int G, const Kv8& kv, int split_req);
+size_t attn_kv8_ws_bytes(int dtype, int C, int K, int Hq, const Kv8& kv, int split_req);
 // Fills the workspace fields and launches; false (message recorded) if it cannot.
 bool attn_kv8(int dtype, AttnKv8Args& a, int split_req, void* ws, cudaStream_t s);
 
