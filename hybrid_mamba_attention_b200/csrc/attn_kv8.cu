@@ -183,23 +183,26 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const AttnKv8Args a
   const bool valid = live && ctx >= 0 && ctx <= (long)a.kv.max_pages * a.kv.page_size;
   // The row's partials q = 0 .. ns - 1 at rows base0 + q * stride.  CUDA-core path: one per
   // split of (c, g).  Tensor-core path: the sequence (c, rb, g) holds t_seq tiles from unit
-  // s0 of the line, which is cut into chunks of Z units; its piece in chunk k has slot
-  // c * spr + rb * Hkv + g + k.
-  int ns = 0;
+  // s0 of the line, which is cut into chunks of Z units; its piece in chunk k0 + p has slot
+  // c * spr + rb * Hkv + g + k0 + p, one partial (pair) or two, q = 2 p + half: half h holds
+  // the piece's tiles of parity h and exists iff the piece has more than h tiles.
+  int ns = 0, s0 = 0, k0 = 0, t_seq = 0, Z = 1;
+  const int halves = a.tc && !a.pair ? 2 : 1;
   size_t base0, stride = R;
   if (a.tc) {
     const int* off = a.sched + 64;
-    const int spr = Hkv * a.n_rb, Z = a.sched[2];
+    const int spr = Hkv * a.n_rb;
     const int rb = row / a.row_block, r = rb * Hkv + g;
-    int k0 = 0;
+    Z = a.sched[2];
     if (valid) {
-      const int tw = (off[c + 1] - off[c]) / spr, t_seq = tw - kAttn8SeqUnits;
-      const int s0 = off[c] + r * tw + kAttn8SeqUnits;
+      const int tw = (off[c + 1] - off[c]) / spr;
+      t_seq = tw - kAttn8SeqUnits;
+      s0 = off[c] + r * tw + kAttn8SeqUnits;
       k0 = s0 / Z;
-      ns = t_seq > 0 ? (s0 + t_seq - 1) / Z - k0 + 1 : 0;
+      ns = t_seq > 0 ? halves * ((s0 + t_seq - 1) / Z - k0 + 1) : 0;
     }
     stride = R < a.row_block ? R : a.row_block;
-    base0 = ((size_t)c * spr + r + k0) * stride + row % a.row_block;
+    base0 = ((size_t)c * spr + r + k0) * halves * stride + row % a.row_block;
   } else {
     ns = valid ? (ctx + (a.kb ? a.K : 0) + a.split_tokens - 1) / a.split_tokens : 0;
     base0 = ((size_t)c * Hkv + g) * a.n_splits * R + row;
@@ -217,6 +220,10 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const AttnKv8Args a
     M = mn;
   };
   for (int q = wq; q < ns; q += W) {
+    if (halves == 2) {
+      const int lo = max(s0, (k0 + (q >> 1)) * Z), hi = min(s0 + t_seq, (k0 + (q >> 1) + 1) * Z);
+      if (hi - lo <= (q & 1)) continue;
+    }
     const size_t b = base0 + (size_t)q * stride;
     const float2 ml = *(const float2*)(a.ws_ml + b * 2);
     const float* acc = a.ws_acc + b * D;

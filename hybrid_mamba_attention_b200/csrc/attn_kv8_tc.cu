@@ -51,6 +51,7 @@ constexpr int TT = kAttn8Tile;  // keys per tile
 constexpr int NPW = 4;          // producer warps
 constexpr int SM_WARP0 = 8;     // first softmax warp (a multiple of 4: warp % 4 is its TMEM quarter)
 constexpr int THREADS = 512;
+constexpr int kFewRegs = 64, kManyRegs = 192;  // per thread: 256 (64 + 192) = 512 * 128, what the launch gives
 constexpr float kPScale = 32.f;   // 2^5: weights enter P times this
 constexpr float kMaxExp = 3.f;    // a weight's exponent may reach this before the maximum moves
 constexpr float kLoScale = 16.f;  // the low part of P is held times this
@@ -70,17 +71,16 @@ __device__ __forceinline__ uint32_t swz(int r, int ch) {
 // the rows' scales (fp32).
 __host__ __device__ inline size_t q_img_bytes(int NR, int D) { return (size_t)NR * (2 * D + 4); }
 
-template <int D, int NR>
+template <int D, int NR, bool PAIR>
 struct Lay {
-  static constexpr int NC = NR / 2;                       // query columns per softmax group
-  static constexpr int PN = NR == 128 ? 256 : 128;        // columns of O^T: hi from 0, lo from PN / 2
-  static constexpr int NQ = NR == 128 ? 1 : 2;            // query buffers
-  static constexpr int Q_BYTES = NR * (2 * D + 4);
+  static constexpr int ROWS = PAIR ? 2 * NR : NR;         // query rows of a sequence
+  static constexpr int PN = 128;                          // columns of O^T: hi from 0, lo from 64
+  static constexpr int NQ = PAIR ? 1 : 2;                 // query buffers
+  static constexpr int Q_BYTES = ROWS * (2 * D + 4);
   static constexpr int Q_BUF = (Q_BYTES + 1023) & ~1023;
   static constexpr int KV = TT * D;                       // one operand of a stage
   static constexpr int STAGE = 2 * KV;
   static constexpr int P_BUF = TT * PN;                   // one byte an element
-  static constexpr int OFF_P = 0;
   static constexpr int OFF_Q = 2 * P_BUF;
   static constexpr int OFF_KV = OFF_Q + NQ * Q_BUF;
   static constexpr int MISC = 6144;
@@ -88,34 +88,44 @@ struct Lay {
   static constexpr int NS = ROOM < 8 ? ROOM : 8;          // K/V ring stages
   static constexpr int OFF_MISC = OFF_KV + NS * STAGE;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
-  static constexpr uint32_t TMEM_COLS = NR == 128 ? 512 : 256;
-  __host__ __device__ static constexpr uint32_t S_COL(int b) { return (uint32_t)(PN + b * NR); }
+  static constexpr uint32_t TMEM_COLS = 512;
+  __host__ __device__ static constexpr uint32_t O_COL(int w) { return (uint32_t)(w * PN); }
+  __host__ __device__ static constexpr uint32_t S_COL(int b) { return (uint32_t)(2 * PN + b * NR); }
   static_assert(NS >= 3, "ring");
-  static_assert(PN + 2 * NR <= (int)TMEM_COLS, "TMEM");
+  static_assert(2 * PN + 4 * NR <= (int)TMEM_COLS, "TMEM");
 };
 
-struct TileMeta {  // written by producer warp 0 before the stage's barrier arrive
-  int end;         // 1: no more work (nothing else is set)
-  int c, g, rb, slot;  // request, kv head, row block; partial slot of the piece
-  int valid;       // keys in the tile
-  int first, last; // first / last tile of its piece
-  int block;       // 1: the block's own keys
-  int joff;        // key i of the tile is seen by the positions j >= joff + i
-  int mixed;       // 1: some key of the tile is hidden from some position
-  int qslot, qpar; // query buffer of the piece and the parity of its load
+enum : int {  // TileMeta::flags
+  kEnd = 1,       // no more work (nothing else is set)
+  kFirst = 2,     // first tile of its piece
+  kLast = 4,      // last tile of its piece
+  kGroupFirst = 8, kGroupLast = 16,  // of its piece's tiles that the same softmax group takes
+  kBlock = 32,    // the block's own keys
+  kMixed = 64,    // some key of the tile is hidden from some position
+  kQPar = 128, kQSlot = 256,         // query buffer of the piece and the parity of its load
+  kHalf = 512,    // odd tile of its piece
+};
+struct alignas(16) TileMeta {  // written by producer warp 0 before the stage's barrier arrive
+  int flags, cg, rb, slot;     // cg = request * Hkv + kv head; row block; the piece's partial slot
+  int valid;                   // keys in the tile
+  int joff;                    // key i of the tile is seen by the positions j >= joff + i
+  int pad[2];
 };
 
 template <int NR>
 struct Misc {
-  uint64_t kv_full[8], kv_empty[8], s_full[2], s_free[2], p_full[2], pv_done[2], q_full[2], q_empty[2], scan[2], drain[2];
+  uint64_t kv_full[8], kv_empty[8], s_full[4], s_free[4], p_full[2], pv_done[2], q_full[2], q_empty[2], drain[2];
   uint32_t tmem;
+  int end_item;             // items from here on do not exist
   TileMeta meta[8];
   float scale[8][16];       // per stage: K scales of its eight 16-key groups, then V scales
-  alignas(16) float2 col[NR];  // (query row's scale, -maximum)
-  alignas(16) float alpha[NR];
-  float m[NR];
-  float cmax[2][4][NR / 2]; // per group and warp: column maxima, later the rows' sums
+  // per softmax group
+  alignas(16) float2 col[2][NR];  // (query row's scale, -maximum)
+  alignas(16) float alpha[2][NR];
+  float m[2][NR];
+  float cmax[2][4][NR];     // per warp: column maxima, later the rows' sums
   float svmax[2][4];
+  uint4 v_nan[8];           // PAIR, per stage: keys whose V row holds a NaN, found by either group
 };
 
 struct Maps {
@@ -251,43 +261,89 @@ __device__ __forceinline__ int float_key(float v) {
 }
 __device__ __forceinline__ float key_float(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 
-template <int D, int NR>
+// One lane of a converged warp (the tensor instructions are issued by it).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
+__device__ __forceinline__ TileMeta load_meta(const TileMeta* m) {
+  TileMeta r;
+  const uint32_t at = tc::smem_u32(m);
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.flags), "=r"(r.cg), "=r"(r.rb), "=r"(r.slot)
+               : "r"(at)
+               : "memory");
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.valid), "=r"(r.joff) : "r"(at + 16) : "memory");
+  return r;
+}
+
+// N consecutive columns of this thread's TMEM lane.
+template <int N>
+__device__ __forceinline__ void ld_columns(uint32_t at, float (&e)[N]) {
+  if constexpr (N == 48) {
+    float a[32], b[16];
+    tc::tmem_ld(at, a);
+    tc::tmem_ld(at + 32, b);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) e[j] = a[j];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) e[32 + j] = b[j];
+  } else {
+    tc::tmem_ld(at, e);
+  }
+}
+
+// An item is one tile's work for one softmax group: item 2 n + w is the n-th of group w.
+// PAIR = false (up to 64 query rows a sequence): the groups take the tiles in turn, item
+// = tile.  PAIR = true (up to 128 rows): each takes one half of the rows of every tile,
+// tile = item / 2, so that a tile's bytes serve both halves.
+template <int D, int NR, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_kv8_tc_kernel(const __grid_constant__ Maps maps, const AttnKv8Args a, float scale_log2, int box_rows) {
-  using L = Lay<D, NR>;
-  constexpr int NS = L::NS, NC = L::NC, PN = L::PN;
+  using L = Lay<D, NR, PAIR>;
+  constexpr int NS = L::NS, PN = L::PN;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023) & ~1023u) - raw);
-  uint8_t* sP = smem + L::OFF_P;
+  uint8_t* sP = smem;
   uint8_t* sQ = smem + L::OFF_Q;
   uint8_t* sKV = smem + L::OFF_KV;
   static_assert(sizeof(Misc<NR>) <= L::MISC, "misc area");
   Misc<NR>& ms = *(Misc<NR>*)(smem + L::OFF_MISC);
-  volatile TileMeta* meta = ms.meta;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hkv = a.kv.Hkv, G = a.Hq / Hkv, R = a.K * G;
-  const int RB = R < NR ? R : NR;  // rows of a partial
+  const int RB = R < L::ROWS ? R : L::ROWS;  // rows of a partial
   int* err = a.err;
   const uint64_t lim = a.wait_ns ? (uint64_t)a.wait_ns : tc::kWaitLimitNs;  // pipeline waits
   constexpr int QK_WARP = 4, PV_WARP = 5;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // for a whole warp
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, err, lim));
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      tc::mbar_init(&ms.kv_full[s], NPW);
+      tc::mbar_init(&ms.kv_full[s], NPW + 4 * NPW);  // a producer lane and four scale lanes a warp
       tc::mbar_init(&ms.kv_empty[s], 1);
     }
+    for (int b = 0; b < 4; ++b) {
+      tc::mbar_init(&ms.s_full[b], 2);  // the product's commit and the issuer's own arrival
+      tc::mbar_init(&ms.s_free[b], 4);
+    }
     for (int b = 0; b < 2; ++b) {
-      tc::mbar_init(&ms.s_full[b], 1);
-      tc::mbar_init(&ms.s_free[b], 8);
-      tc::mbar_init(&ms.p_full[b], 8);
+      tc::mbar_init(&ms.p_full[b], 4);
       tc::mbar_init(&ms.pv_done[b], 1);
       tc::mbar_init(&ms.q_full[b], 1);
       tc::mbar_init(&ms.q_empty[b], 1);
       tc::mbar_init(&ms.drain[b], 1);
-      tc::mbar_init(&ms.scan[b], 4);
     }
+    ms.end_item = 0x7fffffff;
     tc::fence_mbar_init();
   }
   if (warp == QK_WARP) tc::tmem_alloc(&ms.tmem, L::TMEM_COLS);
@@ -298,7 +354,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_wait();  // the previous kernel on the stream is complete from here on
   pdl_trigger();
 
+  // 512 threads launch with 128 registers each; the softmax warps take 64 of the others'
   if (warp < NPW) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     // ------------------------------------------------------------ producers
     // Box bx < nb is rows [bx box_rows, ...) of K, box nb + bx of V, issued by lane bx / 4
     // of warp bx % 4.  Lanes 16..19 of warp w bring the scales of the 16-key groups 2w
@@ -307,7 +365,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int pw = warp, nb = TT / box_rows;
     const int bx = pw + NPW * lane;
     const bool has_box = lane < 16 && bx < 2 * nb;
-    const bool has_scale = lane >= 16 && lane < 20;
+    const bool has_scale = lane >= 16 && lane < 20;  // (16 keys a group)
     const int grp = 2 * pw + (lane & 1);
     const bool is_v = has_scale ? (lane & 2) != 0 : bx >= nb;
     const int sub = has_scale ? 16 * grp : (bx % nb) * box_rows;  // first key of the tile that concerns the lane
@@ -388,26 +446,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         q_last = __shfl_sync(0xffffffffu, q_last, 0);
       }
 
-      // Page ids of the lane's keys two tiles ahead and scales one tile ahead, in
-      // registers (the table index clamped into the request's row: ids past the context's
-      // end are never used).
+      // Page ids of the lane's keys are read three tiles ahead (the table index clamped into
+      // the request's row: ids past the context's end are never used).  The scales are
+      // four-byte asynchronous copies into the stage that the stage's barrier waits for, so
+      // their latency runs beside the pages' own.
       const int32_t* table = a.kv.table + (size_t)c * a.kv.max_pages;
       auto page_of = [&](int local) -> int {
         const int idx = ((lt0 + local) * TT + sub) / page;
         return table[idx < a.kv.max_pages ? idx : a.kv.max_pages - 1];
       };
-      auto scale_of = [&](int pid) -> float {
-        return has_scale && pid >= 0 && pid < a.kv.num_pages ? scales[(size_t)pid * Hkv + g] : 0.f;
-      };
-      int pid0 = page_of(0), pid1 = page_of(1);
-      float sc0 = scale_of(pid0);
+      int pid0 = page_of(0), pid1 = page_of(1), pid2 = page_of(2);
 
       for (int local = 0; local < n_tiles && ok; ++local, ++tile_i) {
         const int pid = pid0;
-        const float sc = sc0;
-        pid0 = pid1;
-        sc0 = scale_of(pid0);
-        pid1 = page_of(local + 2);
+        pid0 = pid1, pid1 = pid2;
+        pid2 = page_of(local + 3);
         const int s = tile_i % NS;
         ok = tc::mbar_wait_warp(&ms.kv_empty[s], ((tile_i / NS) & 1) ^ 1, err, lim);
         if (!ok) break;
@@ -417,14 +470,28 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool block = st >= ct;
         const int t0 = st * TT;
         const int valid = block ? a.K : min(TT, ctx - t0);
-        if (has_scale) ms.scale[s][(is_v ? 8 : 0) + grp] = sc;
+        if (has_scale) {
+          float* to = &ms.scale[s][(is_v ? 8 : 0) + grp];
+          if (block || sub >= valid || pid < 0 || pid >= a.kv.num_pages) {
+            *to = 0.f;
+            tc::mbar_arrive(&ms.kv_full[s]);
+          } else {
+            tc::cp_async4(to, scales + (size_t)pid * Hkv + g);
+            tc::cp_async_arrive(&ms.kv_full[s]);
+          }
+        }
         if (pw == 0 && lane == 0) {
-          volatile TileMeta& m = meta[s];
           const int joff = !a.causal ? -TT : block ? 0 : a.kb ? -TT : max(t0 - ctx + a.K, -TT);
-          m.end = 0, m.c = c, m.g = g, m.rb = rb, m.slot = c * spr + r + k, m.valid = valid;
-          m.first = local == 0, m.last = local == n_tiles - 1, m.block = block;
-          m.joff = joff, m.mixed = joff + valid - 1 > 0;
-          m.qslot = qslot, m.qpar = quse & 1;
+          constexpr int STEP = PAIR ? 1 : 2;  // tiles between those of one group
+          TileMeta m;
+          m.flags = (local == 0 ? kFirst : 0) | (local == n_tiles - 1 ? kLast : 0) | (local < STEP ? kGroupFirst : 0) |
+                    (local >= n_tiles - STEP ? kGroupLast : 0) | (block ? kBlock : 0) |
+                    (joff + valid - 1 > 0 ? kMixed : 0) | (quse & 1 ? kQPar : 0) | (qslot ? kQSlot : 0) |
+                    (local & 1 ? kHalf : 0);
+          m.cg = c * Hkv + g, m.rb = rb, m.slot = c * spr + r + k, m.valid = valid, m.joff = joff;
+          m.pad[0] = m.pad[1] = 0;
+          ms.meta[s] = m;
+          ms.v_nan[s] = make_uint4(0, 0, 0, 0);
         }
         if (block) {
           // the block's K (warp 0) and V (warp 1) images: hi rows, then lo rows
@@ -469,194 +536,242 @@ __global__ void __launch_bounds__(THREADS, 1)
     // sentinel stage: no more work
     if (!stopped) {
       const int s = tile_i % NS;
-      if (tc::mbar_wait_warp(&ms.kv_empty[s], ((tile_i / NS) & 1) ^ 1, err, lim) && lane == 0) {
-        if (pw == 0) meta[s].end = 1;
+      if (tc::mbar_wait_warp(&ms.kv_empty[s], ((tile_i / NS) & 1) ^ 1, err, lim) && (lane == 0 || has_scale)) {
+        if (threadIdx.x == 0) ms.meta[s].flags = kEnd;
         tc::mbar_arrive(&ms.kv_full[s]);
       }
     }
-  } else if (warp == QK_WARP) {
-    if (lane == 0) {
+  } else if (warp < SM_WARP0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    if (warp == QK_WARP) {
       // ---------------------------------------------------------- S^T issuer
-      // S^T_b = K_i . Q^T into S buffer b = i % 2 once tile i has landed, the softmax has
-      // read tile i - 2 out of S_b and the piece's queries are there.
+      // S^T_b = K_i . Q^T into S buffer b = item % 4 once tile i has landed, the softmax has
+      // read item - 4 out of S_b and the piece's queries are there.  Its own arrival on
+      // s_full passes on what it has seen: the tile's description and scales, the queries.
       constexpr uint32_t idesc = tc::idesc_e4m3_f32(TT, NR, false, false);
+      const uint32_t lo_part = (uint32_t)(blk_rows(a.K) * D);
       for (int i = 0;; ++i) {
-        const int s = i % NS, b = i & 1;
-        if (!tc::mbar_wait(&ms.kv_full[s], (i / NS) & 1, err, lim)) break;
-        if (meta[s].end) break;
-        if (meta[s].first && !tc::mbar_wait(&ms.q_full[meta[s].qslot], meta[s].qpar, err, lim)) break;
-        if (i >= 2 && !tc::mbar_wait(&ms.s_free[b], ((i >> 1) - 1) & 1, err, lim)) break;
-        tc::tc_fence_after();
-        const uint32_t q = tc::smem_u32(sQ + meta[s].qslot * L::Q_BUF), kt = tc::smem_u32(sKV + s * L::STAGE);
-        // block tiles: the low parts of K follow its high parts
-        const int parts = meta[s].block ? 2 : 1;
-        for (int p = 0; p < parts; ++p) {
-          const uint32_t kp = kt + p * blk_rows(a.K) * D;
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) {
-            tc::mma_e4m3(tmem + L::S_COL(b), tc::sdesc_b8<D>(kp + kk * 32), tc::sdesc_b8<D>(q + kk * 32), idesc,
-                         (p > 0 || kk > 0) ? 1u : 0u);
-            tc::mma_e4m3(tmem + L::S_COL(b), tc::sdesc_b8<D>(kp + kk * 32), tc::sdesc_b8<D>(q + NR * D + kk * 32),
-                         idesc, 1u);
+        const int s = i % NS;
+        if (!wait(&ms.kv_full[s], (i / NS) & 1)) break;
+        const int flags = load_meta(&ms.meta[s]).flags;
+        const int it0 = PAIR ? 2 * i : i;
+        if (flags & kEnd) {
+          // wake both groups: their next items are it0 and it0 + 1
+          if (lane == 0) *(volatile int*)&ms.end_item = it0;
+          __syncwarp();
+          for (int it = it0; it < it0 + 2; ++it) {
+            if (it >= 4 && !wait(&ms.s_free[it & 3], ((it >> 2) - 1) & 1)) break;
+            if (lane == 0) {
+              tc::mbar_arrive(&ms.s_full[it & 3]);
+              tc::mbar_arrive(&ms.s_full[it & 3]);
+            }
+            __syncwarp();
           }
+          break;
         }
-        tc::mma_commit(&ms.s_full[b]);
+        const int qslot = flags & kQSlot ? 1 : 0;
+        if ((flags & kFirst) && !wait(&ms.q_full[qslot], flags & kQPar ? 1 : 0)) break;
+        bool ok = true;
+        const uint64_t q0 = tc::sdesc_b8<D>(tc::smem_u32(sQ + qslot * L::Q_BUF));
+        const uint64_t k0 = tc::sdesc_b8<D>(tc::smem_u32(sKV + s * L::STAGE));
+        for (int w = 0; w < (PAIR ? 2 : 1) && ok; ++w) {
+          const int it = it0 + w, b = it & 3;
+          if (it >= 4) ok = wait(&ms.s_free[b], ((it >> 2) - 1) & 1);
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (elect_one()) {
+            const uint32_t d = tmem + L::S_COL(b);
+            const uint64_t q = q0 + (uint32_t)(w * NR * D / 16);
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk) {
+              tc::mma_e4m3(d, k0 + 2 * kk, q + 2 * kk, idesc, kk > 0);
+              tc::mma_e4m3(d, k0 + 2 * kk, q + (uint32_t)(L::ROWS * D / 16) + 2 * kk, idesc, 1u);
+            }
+            if (flags & kBlock) {  // the low parts of K follow its high parts
+              const uint64_t kl = k0 + (lo_part >> 4);
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk) {
+                tc::mma_e4m3(d, kl + 2 * kk, q + 2 * kk, idesc, 1u);
+                tc::mma_e4m3(d, kl + 2 * kk, q + (uint32_t)(L::ROWS * D / 16) + 2 * kk, idesc, 1u);
+              }
+            }
+            tc::mma_commit(&ms.s_full[b]);
+            tc::mbar_arrive(&ms.s_full[b]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
       }
       // no MMA or commit arrival may land after the CTA has finished
-      tc::mma_commit(&ms.drain[0]);
+      if (elect_one()) tc::mma_commit(&ms.drain[0]);
+      __syncwarp();
       tc::mbar_wait(&ms.drain[0], 0, err);
-    }
-  } else if (warp == PV_WARP) {
-    if (lane == 0) {
+    } else if (warp == PV_WARP) {
       // ---------------------------------------------------------- O^T issuer
-      // O^T += V_i^T . P_i^T in steps of 32 keys (V rows past the last key are zero) once
-      // P_i is in shared memory; its commit frees the K/V stage (S^T_i finished before
-      // that tile's softmax began) and the P buffer.
+      // O^T_w += V_i^T . P^T in steps of 32 keys (V rows past the last key are zero) once the
+      // item's P is in shared memory; the commit of a tile's last item frees the K/V stage
+      // (its S^T finished before its softmax began).
       constexpr uint32_t idesc = tc::idesc_e4m3_f32(D, PN, true, true);
+      const uint32_t lo_part = (uint32_t)(blk_rows(a.K) * D);
       for (int i = 0;; ++i) {
-        const int s = i % NS, b = i & 1;
-        if (!tc::mbar_wait(&ms.kv_full[s], (i / NS) & 1, err, lim)) break;
-        if (meta[s].end) break;
-        if (!tc::mbar_wait(&ms.p_full[b], (i >> 1) & 1, err, lim)) break;
-        tc::tc_fence_after();
-        const uint32_t p = tc::smem_u32(sP + b * L::P_BUF), vt = tc::smem_u32(sKV + s * L::STAGE + L::KV);
-        const int steps = (meta[s].valid + 31) / 32, parts = meta[s].block ? 2 : 1;
-        for (int h = 0; h < parts; ++h) {
-          const uint32_t vp = vt + h * blk_rows(a.K) * D;
-          for (int kk = 0; kk < steps; ++kk)
-            tc::mma_e4m3(tmem, tc::sdesc_b8<D>(vp + kk * 32 * D), tc::sdesc_b8<128>(p + kk * 32 * 128, TT * 128), idesc,
-                         (h > 0 || kk > 0 || !meta[s].first) ? 1u : 0u);
+        const int s = i % NS;
+        if (!wait(&ms.kv_full[s], (i / NS) & 1)) break;
+        const TileMeta m = load_meta(&ms.meta[s]);
+        if (m.flags & kEnd) break;
+        const uint64_t v0 = tc::sdesc_b8<D>(tc::smem_u32(sKV + s * L::STAGE + L::KV));
+        const int steps = (m.valid + 31) / 32;
+        bool ok = true;
+        for (int j = 0; j < (PAIR ? 2 : 1) && ok; ++j) {
+          const int w = PAIR ? j : i & 1, n = PAIR ? i : i >> 1;
+          ok = wait(&ms.p_full[w], n & 1);
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (elect_one()) {
+            const uint32_t d = tmem + L::O_COL(w);
+            const uint64_t p = tc::sdesc_b8<128>(tc::smem_u32(sP + w * L::P_BUF));
+            const uint32_t acc0 = m.flags & kGroupFirst ? 0u : 1u;
+#pragma unroll
+            for (int kk = 0; kk < TT / 32; ++kk)
+              if (kk < steps) tc::mma_e4m3(d, v0 + kk * (32 * D / 16), p + kk * (32 * 128 / 16), idesc, kk > 0 ? 1u : acc0);
+            if (m.flags & kBlock) {  // the low parts of V follow its high parts
+              const uint64_t vl = v0 + (lo_part >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk)
+                if (kk < steps) tc::mma_e4m3(d, vl + kk * (32 * D / 16), p + kk * (32 * 128 / 16), idesc, 1u);
+            }
+            if (!PAIR || j == 1) {
+              if (m.flags & kLast) tc::mbar_arrive(&ms.q_empty[m.flags & kQSlot ? 1 : 0]);
+              tc::mma_commit(&ms.kv_empty[s]);
+            }
+            tc::mma_commit(&ms.pv_done[w]);
+          }
+          __syncwarp();
         }
-        if (meta[s].last) tc::mbar_arrive(&ms.q_empty[meta[s].qslot]);
-        tc::mma_commit(&ms.kv_empty[s]);
-        tc::mma_commit(&ms.pv_done[b]);
+        if (!ok) break;
       }
-      tc::mma_commit(&ms.drain[1]);
+      if (elect_one()) tc::mma_commit(&ms.drain[1]);
+      __syncwarp();
       tc::mbar_wait(&ms.drain[1], 0, err);
     }
-  } else if (warp >= SM_WARP0) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
     // ------------------------------------------------------------ softmax groups
-    // Group w holds the query columns [w NC, (w + 1) NC); the thread's key is its lane of
-    // the tile.  A wait that gave up (ok = false) is acted on only at the group's barriers,
-    // so that all four warps leave together.
+    // The thread's key is its lane of the tile; it holds all NR columns of its group's item.
+    // A wait that gave up (ok = false) is acted on only at the group's barriers, so that
+    // all four warps leave together.
     const int w = (warp - SM_WARP0) >> 2, quarter = warp & 3;
     const int key = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t t_hi = tmem + lane_off + w * NC, t_lo = t_hi + PN / 2;
+    const uint32_t t_hi = tmem + lane_off + L::O_COL(w), t_lo = t_hi + PN / 2;
+    float2* col = ms.col[w];
+    float* alpha = ms.alpha[w];
     auto group_or = [&](bool p) -> bool {
       return w == 0 ? tc::bar_or<2, 128>(p) : tc::bar_or<3, 128>(p);
     };
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, err, lim));
-    };
-    float l[NC];        // this key lane's share of the columns' sums
+    float l[NR];        // this key lane's share of the columns' sums
     float Mv = 0.f, inv_mv = 0.f;  // largest V scale of the piece, 1 / it
     bool ok = true;
-    uint32_t scans = 0;  // bit b: parity of the scans of tiles i = b (mod 2)
     // the previous piece's partial, still in O^T
     bool pend = false;
     size_t pend_base = 0;
-    int pend_rows = 0, pend_i = 0;
+    int pend_rows = 0;
     float pend_mul = 0.f;
-    // O^T after the product of tile i, times mul, to rows base.. of the workspace
-    auto write_partial = [&](int i, size_t base, int rows, float mul) -> bool {
-      if (!wait(&ms.pv_done[i & 1], (i >> 1) & 1)) return false;
+    // O^T (every product issued into it has finished) to the workspace
+    auto write_partial = [&]() {
       tc::tc_fence_after();
       const int d = D == 128 ? key : quarter * 16 + lane;
       const bool on = D == 128 || lane < 16;
-      constexpr int CH = NC < 16 ? NC : 16;
 #pragma unroll
-      for (int j0 = 0; j0 < NC; j0 += CH) {
-        float hi[CH], lo[CH];
+      for (int j0 = 0; j0 < NR; j0 += 16) {
+        float hi[16], lo[16];
         tc::tmem_ld(t_hi + j0, hi);
         tc::tmem_ld(t_lo + j0, lo);
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
-          if (on && w * NC + j0 + j < rows)
-            a.ws_acc[(base + w * NC + j0 + j) * D + d] = fmaf(lo[j], 1.f / kLoScale, hi[j]) * mul;
+        for (int j = 0; j < 16; ++j)
+          if (on && j0 + j < pend_rows)
+            a.ws_acc[(pend_base + j0 + j) * D + d] = fmaf(lo[j], 1.f / kLoScale, hi[j]) * pend_mul;
       }
-      return true;
+      pend = false;
     };
 
-    for (int i = 0;; ++i) {
-      const int s = i % NS, b = i & 1;
-      bool end = false;
-      if (ok) {
-        ok = wait(&ms.kv_full[s], (i / NS) & 1);
-        end = ok && meta[s].end != 0;
-        if (ok && !end) ok = wait(&ms.s_full[b], (i >> 1) & 1);
-      }
-      const bool run = ok && !end;
-      bool first = false, last = false, mixed = false, block = false;
-      int valid = 0, cmin = 0, rb = 0, slot = 0;
+    int n = 0;  // items of the group so far
+    for (;; ++n) {
+      const int it = 2 * n + w, b = it & 3, s = (PAIR ? n : it) % NS;
+      if (ok) ok = wait(&ms.s_full[b], (it >> 2) & 1);
+      const bool run = ok && it < *(volatile int*)&ms.end_item;
+      TileMeta m = {};
+      int cmin = 0;
+      bool first = false;
       const float* cq_first = nullptr;
-      float e[NC], sv = 0.f;
+      float e[NR], sv = 0.f;
       float e_max = -INFINITY;
       if (run) {
-        first = meta[s].first != 0, mixed = meta[s].mixed != 0, block = meta[s].block != 0;
-        last = meta[s].last != 0, valid = meta[s].valid, rb = meta[s].rb, slot = meta[s].slot;
+        m = load_meta(&ms.meta[s]);
+        first = (m.flags & kGroupFirst) != 0;
+        float ck = 0.f;
+        if (key < m.valid) {
+          if (m.flags & kBlock) {
+            const float* bs = a.blk_scale + (size_t)m.cg * 2 * kBlkRows;
+            ck = bs[key], sv = bs[kBlkRows + key];
+          } else {
+            ck = ms.scale[s][key >> 4], sv = ms.scale[s][8 + (key >> 4)];
+          }
+        }
+        ck *= scale_log2;
+        // columns below cmin do not see this key (row = rb ROWS + column, position row / G)
+        cmin = key >= m.valid ? NR : max(m.joff + key, 0) * G - m.rb * L::ROWS - (PAIR ? w * NR : 0);
         tc::tc_fence_after();
-        tc::tmem_ld(tmem + lane_off + L::S_COL(b) + w * NC, e);
+        ld_columns<NR>(tmem + lane_off + L::S_COL(b), e);
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ms.s_free[b]);
-        float ck = 0.f;
-        if (block) {
-          const float* bs = a.blk_scale + (size_t)(meta[s].c * Hkv + meta[s].g) * 2 * kBlkRows;
-          if (key < valid) ck = bs[key], sv = bs[kBlkRows + key];
-        } else if (key < valid) {
-          ck = ms.scale[s][key >> 4], sv = ms.scale[s][8 + (key >> 4)];
-        }
-        ck *= scale_log2;
-        // columns below cmin do not see this key (row = rb NR + column, position row / G)
-        cmin = key >= valid ? NR : max(meta[s].joff + key, 0) * G - rb * NR;
-        if (first) {
-          ok = wait(&ms.q_full[meta[s].qslot], meta[s].qpar);
-          cq_first = (const float*)(sQ + meta[s].qslot * L::Q_BUF + 2 * NR * D) + w * NC;
-        }
         const float2 ck2 = make_float2(ck, ck);
+        if (first) {
+          cq_first = (const float*)(sQ + (m.flags & kQSlot ? L::Q_BUF : 0) + 2 * L::ROWS * D) + (PAIR ? w * NR : 0);
 #pragma unroll
-        for (int j = 0; j < NC; j += 2) {
-          const float2 u = tc::fmul2(make_float2(e[j], e[j + 1]), ck2);
-          if (first) {
-            e[j] = u.x * cq_first[j], e[j + 1] = u.y * cq_first[j + 1];
-          } else {
-            const float4 cm = *(const float4*)&ms.col[w * NC + j];
-            const float2 x = tc::ffma2(u, make_float2(cm.x, cm.z), make_float2(cm.y, cm.w));
+          for (int j = 0; j < NR; ++j) e[j] *= ck * cq_first[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < NR; j += 2) {
+            const float4 cm = *(const float4*)&col[j];
+            const float2 x = tc::ffma2(tc::fmul2(make_float2(e[j], e[j + 1]), ck2), make_float2(cm.x, cm.z),
+                                       make_float2(cm.y, cm.w));
             e[j] = x.x, e[j + 1] = x.y;
           }
         }
-        if (cmin > w * NC) {
+        if (cmin > 0) {
 #pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (w * NC + j < cmin) e[j] = -INFINITY;
+          for (int j = 0; j < NR; ++j)
+            if (j < cmin) e[j] = -INFINITY;
         }
+        float mx[4] = {e[0], e[1], e[2], e[3]};
 #pragma unroll
-        for (int j = 0; j < NC; ++j) e_max = fmaxf(e_max, e[j]);
+        for (int j = 4; j < NR; j += 4)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], e[j + k]);
+        e_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       }
-      if (group_or(!run || !ok || first || e_max > kMaxExp || sv > Mv)) {
+      if (group_or(!run || first || e_max > kMaxExp || sv > Mv)) {
         // The maxima move (or the group leaves).  s = e + m (e alone in a first tile).
         if (run) {
 #pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            const float v = first ? e[j] : e[j] - ms.col[w * NC + j].y;
-            e[j] = v;
-            const int top = __reduce_max_sync(0xffffffffu, float_key(v));
+          for (int j = 0; j < NR; ++j) {
+            if (!first) e[j] -= col[j].y;
+            const int top = __reduce_max_sync(0xffffffffu, float_key(e[j]));
             if (lane == (j & 31)) ms.cmax[w][quarter][j] = key_float(top);
           }
           const float t = warp_max(sv);
           if (lane == 0) ms.svmax[w][quarter] = t;
         }
-        if (group_or(!run || !ok)) break;
+        if (group_or(!run)) break;
         if (quarter == 0) {
-          for (int j = lane; j < NC; j += 32) {
+          for (int j = lane; j < NR; j += 32) {
             const float cm = fmaxf(fmaxf(ms.cmax[w][0][j], ms.cmax[w][1][j]), fmaxf(ms.cmax[w][2][j], ms.cmax[w][3][j]));
-            const int col = w * NC + j;
-            const float m_old = first ? -INFINITY : ms.m[col], m_new = fmaxf(m_old, cm);
-            const float cq = first ? cq_first[j] : ms.col[col].x;
-            ms.m[col] = m_new;
-            ms.col[col] = make_float2(cq, m_new == -INFINITY ? 0.f : -m_new);
-            ms.alpha[col] = m_old == -INFINITY ? 1.f : exp2f(m_old - m_new);
+            const float m_old = first ? -INFINITY : ms.m[w][j], m_new = fmaxf(m_old, cm);
+            const float cq = first ? cq_first[j] : col[j].x;
+            ms.m[w][j] = m_new;
+            col[j] = make_float2(cq, m_new == -INFINITY ? 0.f : -m_new);
+            alpha[j] = m_old == -INFINITY ? 1.f : exp2f(m_old - m_new);
           }
         }
         const float sv_top = fmaxf(fmaxf(ms.svmax[w][0], ms.svmax[w][1]), fmaxf(ms.svmax[w][2], ms.svmax[w][3]));
@@ -667,141 +782,131 @@ __global__ void __launch_bounds__(THREADS, 1)
         group_or(false);  // col, m and alpha are written
         if (first) {
 #pragma unroll
-          for (int j = 0; j < NC; ++j) l[j] = 0.f;
+          for (int j = 0; j < NR; ++j) l[j] = 0.f;
         } else {
 #pragma unroll
-          for (int j = 0; j < NC; ++j) l[j] *= ms.alpha[w * NC + j];
-          // O^T holds the piece's earlier tiles once the product of tile i - 1 is done
-          ok = wait(&ms.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
+          for (int j = 0; j < NR; ++j) l[j] *= alpha[j];
+          // O^T holds the group's earlier tiles of the piece once its last product is done
+          ok = wait(&ms.pv_done[w], (n - 1) & 1);
           if (ok) {
             tc::tc_fence_after();
-            constexpr int CH = 8;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int j0 = 0; j0 < NC; j0 += CH) {
-                float o[CH];
+              for (int j0 = 0; j0 < NR; j0 += 8) {
+                float o[8];
                 const uint32_t t = (h ? t_lo : t_hi) + j0;
                 tc::tmem_ld(t, o);
 #pragma unroll
-                for (int j = 0; j < CH; ++j) o[j] *= ms.alpha[w * NC + j0 + j] * mv_ratio;
+                for (int j = 0; j < 8; ++j) o[j] *= alpha[j0 + j] * mv_ratio;
                 tc::tmem_st8(t, o);
               }
           }
         }
 #pragma unroll
-        for (int j = 0; j < NC; ++j) e[j] += ms.col[w * NC + j].y;
+        for (int j = 0; j < NR; ++j) e[j] += col[j].y;
       }
       // From here on a failed wait only skips work; the group leaves at the next barrier.
-      const float rv = sv * inv_mv * kPScale;
-      uint32_t hi[NC / 4], lo[NC / 4];
-#pragma unroll
-      for (int j = 0; j < NC; j += 4) {
-        uint32_t hh[2], ll[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float2 p = make_float2(tc::ex2_ftz(e[j + 2 * k]), tc::ex2_ftz(e[j + 2 * k + 1]));
-          const float2 ls = tc::fadd2(make_float2(l[j + 2 * k], l[j + 2 * k + 1]), p);
-          l[j + 2 * k] = ls.x, l[j + 2 * k + 1] = ls.y;
-          const float2 pv = tc::fmul2(p, make_float2(rv, rv));
-          // fp16 first (11 bits, well below the two parts' error): the parts' differences
-          // are then packed half arithmetic
-          const __half2 ph = __floats2half2_rn(pv.x, pv.y);
-          hh[k] = e4m3x2_h(ph);
-          const __half2 d = __hfma2(ph, __float2half2_rn(kLoScale), __hmul2(e4m3x2_to_h2(hh[k]), __float2half2_rn(-kLoScale)));
-          ll[k] = e4m3x2_h(d);
-        }
-        hi[j / 4] = hh[0] | (hh[1] << 16);
-        lo[j / 4] = ll[0] | (ll[1] << 16);
-      }
-      // The P buffer is free once the product of tile i - 2 is done.  (Before the scan: a
-      // group's scan of tile i + 2 then follows both groups' scans of tile i, and the
-      // phases of a scan barrier stay at most one ahead of its waiter.)
-      if (ok && i >= 2) ok = wait(&ms.pv_done[b], ((i >> 1) - 1) & 1);
-      // a NaN in a V row that some column does not see: the product would carry it into
-      // that column, too, so the row is cleared and the columns that see it get a NaN sum
-      bool bad = false;
+      // The group's last product is done: its P buffer is free, and O^T is complete if the
+      // previous piece's partial is still to be written (before this item's product may
+      // overwrite it).
+      if (ok && n > 0) ok = wait(&ms.pv_done[w], (n - 1) & 1);
+      if (ok && pend) write_partial();
       uint8_t* v_row = sKV + s * L::STAGE + L::KV + key * D;
-      if (ok && mixed) {
-        if (key < valid) {
-          const int n16 = D / 16;
-          for (int h = 0; h < (block ? 2 : 1); ++h)
-            for (int q = 0; q < n16; ++q) {
+      if (m.flags & kMixed) {
+        // a NaN in a V row that some column does not see: the product would carry it into
+        // that column, too, so the row is cleared and the columns that see it get a NaN sum.
+        // PAIR: the other group may have cleared the row already, and has then marked it
+        // before.
+        bool bad = false;
+        if (key < m.valid)
+          for (int h = 0; h < (m.flags & kBlock ? 2 : 1); ++h)
+            for (int q = 0; q < D / 16; ++q) {
               const uint4 x = *(const uint4*)(v_row + h * blk_rows(a.K) * D + q * 16);
               const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int z = 0; z < 4; ++z) bad = bad || __vcmpeq4(xs[z] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
             }
+        if constexpr (PAIR) {
+          volatile uint32_t* mark = &ms.v_nan[s].x + quarter;
+          if (bad) atomicOr((uint32_t*)mark, 1u << lane);
+          __threadfence_block();
+          bad = bad || (*mark >> lane & 1) != 0;
         }
-        if (w == 1) {
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&ms.scan[b]);
-        } else {
-          ok = wait(&ms.scan[b], (scans >> b) & 1);  // the other group has read the rows
-          if (ok && bad)
-            for (int h = 0; h < (block ? 2 : 1); ++h)
-              for (int q = 0; q < D / 16; ++q)
-                *(uint4*)(v_row + h * blk_rows(a.K) * D + q * 16) = make_uint4(0, 0, 0, 0);
-        }
-        scans ^= 1u << b;
-        if (bad)
+        if (bad) {
+          for (int h = 0; h < (m.flags & kBlock ? 2 : 1); ++h)
+            for (int q = 0; q < D / 16; ++q)
+              *(uint4*)(v_row + h * blk_rows(a.K) * D + q * 16) = make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (w * NC + j >= cmin) l[j] = __int_as_float(0x7fffffff);
+          for (int j = 0; j < NR; ++j)
+            if (j >= cmin) l[j] = __int_as_float(0x7fffffff);
+        }
       }
       // V rows past the last key may hold anything (their weights are 0): clear them
-      if (ok && !block && key >= valid && key < ((valid + 31) & ~31)) {
+      if (!(m.flags & kBlock) && key >= m.valid && key < ((m.valid + 31) & ~31)) {
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) *(uint4*)(v_row + w * (D / 2) + q * 16) = make_uint4(0, 0, 0, 0);
+        for (int q = 0; q < D / 16; ++q) *(uint4*)(v_row + q * 16) = make_uint4(0, 0, 0, 0);
       }
-      if (ok) {
-        uint8_t* prow = sP + b * L::P_BUF + key * 128;
-        auto put = [&](const uint32_t (&x)[NC / 4], uint8_t* base, int byte0) {
-          if constexpr (NC >= 16) {
+      const float rv = sv * inv_mv * kPScale;
+      const float2 rv2 = make_float2(rv, rv);
+      uint8_t* prow = sP + w * L::P_BUF + key * 128;
 #pragma unroll
-            for (int q = 0; q < NC / 16; ++q)
-              *(uint4*)(base + (((byte0 / 16 + q) ^ (key & 7)) << 4)) =
-                  make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-          } else {
-            *(uint2*)(base + (((byte0 / 16) ^ (key & 7)) << 4) + (byte0 & 15)) = make_uint2(x[0], x[1]);
+      for (int j0 = 0; j0 < NR; j0 += 16) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t hh[2], ll[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int j = j0 + 4 * q + 2 * k;
+            const float2 p = make_float2(tc::ex2_ftz(e[j]), tc::ex2_ftz(e[j + 1]));
+            const float2 ls = tc::fadd2(make_float2(l[j], l[j + 1]), p);
+            l[j] = ls.x, l[j + 1] = ls.y;
+            const float2 pv = tc::fmul2(p, rv2);
+            // fp16 first (11 bits, well below the two parts' error): the parts' difference
+            // is then packed half arithmetic
+            const __half2 ph = __floats2half2_rn(pv.x, pv.y);
+            hh[k] = e4m3x2_h(ph);
+            ll[k] = e4m3x2_h(__hmul2(__hsub2(ph, e4m3x2_to_h2(hh[k])), __float2half2_rn(kLoScale)));
           }
-        };
-        put(hi, prow, w * NC);
-        if constexpr (NR == 128) put(lo, prow + TT * 128, w * NC);
-        else put(lo, prow, 64 + w * NC);
+          hi[q] = hh[0] | (hh[1] << 16);
+          lo[q] = ll[0] | (ll[1] << 16);
+        }
+        if (ok) {
+          *(uint4*)(prow + (((j0 / 16) ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *(uint4*)(prow + (((4 + j0 / 16) ^ (key & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
       }
       tc::fence_proxy_async();
-      // the previous piece's partial, before this tile's product may overwrite O^T
-      if (ok && pend) ok = write_partial(pend_i, pend_base, pend_rows, pend_mul);
-      pend = false;
       tc::tc_fence_before();
       __syncwarp();
-      if (ok && lane == 0) tc::mbar_arrive(&ms.p_full[b]);
+      if (ok && lane == 0) tc::mbar_arrive(&ms.p_full[w]);
 
-      if (last) {
-        // the piece is complete: its sums now, its O^T during the next tile
-        const int rows = min(RB, R - rb * NR);
-        const size_t base = (size_t)slot * RB;
+      if (m.flags & kGroupLast) {
+        // the group's part of the piece is complete: its sums now, its O^T during the next
+        // item
+        const int rows = min(NR, min(L::ROWS, R - m.rb * L::ROWS) - (PAIR ? w * NR : 0));
+        const size_t base =
+            PAIR ? (size_t)m.slot * RB + w * NR : ((size_t)m.slot * 2 + (m.flags & kHalf ? 1 : 0)) * RB;
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
+        for (int j = 0; j < NR; ++j) {
           const float t = warp_sum(l[j]);
           if (lane == (j & 31)) ms.cmax[w][quarter][j] = t;
         }
         group_or(false);
         if (quarter == 0) {
-          for (int j = lane; j < NC; j += 32)
-            if (w * NC + j < rows) {
-              float* ml = a.ws_ml + (base + w * NC + j) * 2;
-              ml[0] = ms.m[w * NC + j];
-              ml[1] = (ms.cmax[w][0][j] + ms.cmax[w][1][j]) + (ms.cmax[w][2][j] + ms.cmax[w][3][j]);
-            }
+          for (int j = lane; j < rows; j += 32) {
+            float* ml = a.ws_ml + (base + j) * 2;
+            ml[0] = ms.m[w][j];
+            ml[1] = (ms.cmax[w][0][j] + ms.cmax[w][1][j]) + (ms.cmax[w][2][j] + ms.cmax[w][3][j]);
+          }
         }
         group_or(false);  // cmax and m may be written again
-        pend = true, pend_i = i, pend_base = base, pend_rows = rows;
+        pend = true, pend_base = base, pend_rows = rows;
         pend_mul = Mv * (1.f / kPScale);
       }
     }
-    if (ok && pend) write_partial(pend_i, pend_base, pend_rows, pend_mul);
+    if (ok && pend && wait(&ms.pv_done[w], (n - 1) & 1)) write_partial();  // the last piece's
     tc::tc_fence_before();
   }
   __syncthreads();
@@ -843,11 +948,11 @@ bool make_map(CUtensorMap* m, const Kv8& kv, const uint8_t* base, int box_rows) 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NR>
+template <int D, int NR, bool PAIR>
 bool launch(const AttnKv8Args& a, int grid, cudaStream_t s) {
-  using L = Lay<D, NR>;
-  if (cudaFuncSetAttribute(attn_kv8_tc_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) !=
-      cudaSuccess) {
+  using L = Lay<D, NR, PAIR>;
+  auto kernel = attn_kv8_tc_kernel<D, NR, PAIR>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess) {
     set_error("cudaFuncSetAttribute(attn_kv8_tc_kernel) failed");
     return false;
   }
@@ -859,7 +964,7 @@ bool launch(const AttnKv8Args& a, int grid, cudaStream_t s) {
     return false;
   }
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
-  launch_pdl(attn_kv8_tc_kernel<D, NR>, grid, THREADS, L::SMEM, s, maps, a, scale_log2, box_rows);
+  launch_pdl(kernel, grid, THREADS, L::SMEM, s, maps, a, scale_log2, box_rows);
   note_launch();
   return true;
 }
@@ -873,11 +978,12 @@ bool launch_d(const AttnKv8Args& a, cudaStream_t s) {
   const long rows = (long)a.C * a.kv.Hkv * a.n_rb * a.row_block + (a.kb ? (long)a.C * a.kv.Hkv * 2 * blk_rows(a.K) : 0);
   launch_pdl(attn_kv8_prep_kernel<D>, 1 + (unsigned)((rows + 7) / 8), 256, 0, s, a, grid);
   note_launch();
+  if (a.pair) return a.row_block == 96 ? launch<D, 48, true>(a, grid, s) : launch<D, 64, true>(a, grid, s);
   switch (a.row_block) {
-    case 16: return launch<D, 16>(a, grid, s);
-    case 32: return launch<D, 32>(a, grid, s);
-    case 64: return launch<D, 64>(a, grid, s);
-    default: return launch<D, 128>(a, grid, s);
+    case 16: return launch<D, 16, false>(a, grid, s);
+    case 32: return launch<D, 32, false>(a, grid, s);
+    case 48: return launch<D, 48, false>(a, grid, s);
+    default: return launch<D, 64, false>(a, grid, s);
   }
 }
 
@@ -891,14 +997,16 @@ bool attn_kv8_tc_shape(int dtype, int D, int page_size) {
 
 size_t attn_kv8_tc_plan(AttnKv8Args& a, int split_req, void* ws) {
   const int D = a.kv.D, Hkv = a.kv.Hkv, R = a.K * (a.Hq / Hkv);
-  // the narrowest N that holds the rows: the tensor time, the exponentials and the
-  // barrier work of a tile all go by it
-  a.row_block = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
-  a.n_rb = cdiv(R, a.row_block);
+  // The columns of a softmax group in 16s: the tensor time, the exponentials and the
+  // registers all go by them.  Up to 64 rows the two groups take tiles in turn; more rows
+  // are two halves of up to 64 that the groups take from every tile, in blocks of 128.
+  a.pair = R > 64;
+  a.n_rb = cdiv(R, 128);
+  a.row_block = a.pair ? 32 * cdiv(cdiv(R, a.n_rb), 32) : 16 * cdiv(R, 16);
   a.chunk_units = split_req > 0 ? cdiv(split_req, TT) : 0;
   a.max_chunks = a.chunk_units > 0 ? kMaxChunksExplicit : kMaxChunksAuto;
   const size_t seqs = (size_t)a.C * Hkv * a.n_rb;
-  const size_t rows = (seqs + a.max_chunks) * (R < a.row_block ? R : a.row_block);
+  const size_t rows = (seqs + a.max_chunks) * (a.pair ? 1 : 2) * (R < a.row_block ? R : a.row_block);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     uint8_t* p = (uint8_t*)ws + off;
