@@ -48,10 +48,12 @@ namespace hspec {
 namespace {
 
 constexpr int TT = kAttn8Tile;  // keys per tile
-constexpr int NPW = 4;          // producer warps
-constexpr int SM_WARP0 = 8;     // first softmax warp (a multiple of 4: warp % 4 is its TMEM quarter)
-constexpr int THREADS = 512;
-constexpr int kFewRegs = 64, kManyRegs = 192;  // per thread: 256 (64 + 192) = 512 * 128, what the launch gives
+constexpr int NPW = 2;          // producer warps
+constexpr int SM_WARP0 = 4;     // first softmax warp (a multiple of 4: warp % 4 is its TMEM quarter)
+constexpr int SMW = 16;         // softmax warps: four groups of four
+constexpr int THREADS = 32 * (SM_WARP0 + SMW);
+// registers per thread after the launch's 96: 128 * 56 + 512 * 104 <= 640 * 96
+constexpr int kFewRegs = 56, kManyRegs = 104;
 constexpr float kPScale = 32.f;   // 2^5: weights enter P times this
 constexpr float kMaxExp = 3.f;    // a weight's exponent may reach this before the maximum moves
 constexpr float kLoScale = 16.f;  // the low part of P is held times this
@@ -83,7 +85,7 @@ struct Lay {
   static constexpr int P_BUF = TT * PN;                   // one byte an element
   static constexpr int OFF_Q = 2 * P_BUF;
   static constexpr int OFF_KV = OFF_Q + NQ * Q_BUF;
-  static constexpr int MISC = 6144;
+  static constexpr int MISC = 5632;
   static constexpr int ROOM = (227 * 1024 - 1024 - MISC - OFF_KV) / STAGE;
   static constexpr int NS = ROOM < 8 ? ROOM : 8;          // K/V ring stages
   static constexpr int OFF_MISC = OFF_KV + NS * STAGE;
@@ -120,12 +122,12 @@ struct Misc {
   TileMeta meta[8];
   float scale[8][16];       // per stage: K scales of its eight 16-key groups, then V scales
   // per softmax group
-  alignas(16) float2 col[2][NR];  // (query row's scale, -maximum)
-  alignas(16) float alpha[2][NR];
-  float m[2][NR];
-  float cmax[2][4][NR];     // per warp: column maxima, later the rows' sums
-  float svmax[2][4];
-  uint4 v_nan[8];           // PAIR, per stage: keys whose V row holds a NaN, found by either group
+  alignas(16) float2 col[4][NR / 2];  // (query row's scale, -maximum)
+  alignas(16) float alpha[4][NR / 2];
+  float m[4][NR / 2];
+  float cmax[4][4][NR / 2]; // per warp: column maxima, later the rows' sums
+  float svmax[4][4];
+  uint4 v_nan[8];           // per stage: keys whose V row holds a NaN, as the groups find it
 };
 
 struct Maps {
@@ -286,14 +288,14 @@ __device__ __forceinline__ TileMeta load_meta(const TileMeta* m) {
 // N consecutive columns of this thread's TMEM lane.
 template <int N>
 __device__ __forceinline__ void ld_columns(uint32_t at, float (&e)[N]) {
-  if constexpr (N == 48) {
-    float a[32], b[16];
+  if constexpr (N == 24) {
+    float a[16], b[8];
     tc::tmem_ld(at, a);
-    tc::tmem_ld(at + 32, b);
+    tc::tmem_ld(at + 16, b);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) e[j] = a[j];
+    for (int j = 0; j < 16; ++j) e[j] = a[j];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) e[32 + j] = b[j];
+    for (int j = 0; j < 8; ++j) e[16 + j] = b[j];
   } else {
     tc::tmem_ld(at, e);
   }
@@ -307,7 +309,7 @@ template <int D, int NR, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_kv8_tc_kernel(const __grid_constant__ Maps maps, const AttnKv8Args a, float scale_log2, int box_rows) {
   using L = Lay<D, NR, PAIR>;
-  constexpr int NS = L::NS, PN = L::PN;
+  constexpr int NS = L::NS, PN = L::PN, NC = NR / 2;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023) & ~1023u) - raw);
@@ -322,22 +324,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int RB = R < L::ROWS ? R : L::ROWS;  // rows of a partial
   int* err = a.err;
   const uint64_t lim = a.wait_ns ? (uint64_t)a.wait_ns : tc::kWaitLimitNs;  // pipeline waits
-  constexpr int QK_WARP = 4, PV_WARP = 5;
+  constexpr int QK_WARP = NPW, PV_WARP = NPW + 1;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // for a whole warp
     return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, err, lim));
   };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      tc::mbar_init(&ms.kv_full[s], NPW + 4 * NPW);  // a producer lane and four scale lanes a warp
+      tc::mbar_init(&ms.kv_full[s], NPW + 16);  // a lane of each producer warp, the scale lanes
       tc::mbar_init(&ms.kv_empty[s], 1);
     }
     for (int b = 0; b < 4; ++b) {
       tc::mbar_init(&ms.s_full[b], 2);  // the product's commit and the issuer's own arrival
-      tc::mbar_init(&ms.s_free[b], 4);
+      tc::mbar_init(&ms.s_free[b], 8);
     }
     for (int b = 0; b < 2; ++b) {
-      tc::mbar_init(&ms.p_full[b], 4);
+      tc::mbar_init(&ms.p_full[b], 8);
       tc::mbar_init(&ms.pv_done[b], 1);
       tc::mbar_init(&ms.q_full[b], 1);
       tc::mbar_init(&ms.q_empty[b], 1);
@@ -358,16 +360,17 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp < NPW) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     // ------------------------------------------------------------ producers
-    // Box bx < nb is rows [bx box_rows, ...) of K, box nb + bx of V, issued by lane bx / 4
-    // of warp bx % 4.  Lanes 16..19 of warp w bring the scales of the 16-key groups 2w
-    // and 2w + 1 (K, K, V, V).  All producer warps walk the same tiles; warp 0 loads the
-    // queries and describes the tile.
+    // Box bx < nb is rows [bx box_rows, ...) of K, box nb + bx of V, issued by lane
+    // bx / NPW of warp bx % NPW.  SL lanes from 16 on bring the scales of 16-key groups, half
+    // of them K's.  All producer warps walk the same tiles; warp 0 loads the queries and
+    // describes the tile.
     const int pw = warp, nb = TT / box_rows;
     const int bx = pw + NPW * lane;
+    constexpr int SL = 16 / NPW;
     const bool has_box = lane < 16 && bx < 2 * nb;
-    const bool has_scale = lane >= 16 && lane < 20;  // (16 keys a group)
-    const int grp = 2 * pw + (lane & 1);
-    const bool is_v = has_scale ? (lane & 2) != 0 : bx >= nb;
+    const bool has_scale = lane >= 16 && lane < 16 + SL;
+    const int grp = pw * (SL / 2) + (lane & (SL / 2 - 1));
+    const bool is_v = has_scale ? (lane & (SL / 2)) != 0 : bx >= nb;
     const int sub = has_scale ? 16 * grp : (bx % nb) * box_rows;  // first key of the tile that concerns the lane
     const float* scales = is_v ? a.kv.vs : a.kv.ks;
     if (threadIdx.x == 0) {
@@ -392,26 +395,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     int k = blockIdx.x;  // this CTA's chunk
     int pos = k < n_chunks ? k * Z : 0, end = k < n_chunks ? min(T, pos + Z) : 0;
     int c = pos < end ? locate(pos) : 0;
-    int tile_i = 0;   // tiles this warp has armed (its arrival on their stage)
-    int q_last = -1;  // warp 0: the last piece whose queries it armed
-    bool ok = true;
-    // Every producer warp walks the same pieces and passes the same barriers: the loop
-    // ends only at one, when the work is done or a producer has given up waiting.
-    bool stopped = false;
-    for (int seq = 0;; ++seq) {
-      if (tc::bar_or<1, 32 * NPW>(!ok)) {
-        stopped = true;
-        break;
-      }
-      int r = 0, lt0 = 0, n_tiles = 0;
-      bool done = false;
-      while (n_tiles == 0) {
+    // The next piece: tiles [lt0, lt0 + n) of sequence r of request c within the chunk (a
+    // span that holds only a sequence's start units has no tiles and is passed over); n = 0
+    // at the end.
+    struct Piece {
+      int c, r, k, lt0, n, ctx;
+    };
+    auto advance = [&]() -> Piece {
+      Piece q = {0, 0, 0, 0, 0, 0};
+      while (q.n == 0) {
         if (pos >= end) {  // the CTA's next chunk
           k += gridDim.x;
-          if (k >= n_chunks) {
-            done = true;
-            break;
-          }
+          if (k >= n_chunks) return q;
           pos = k * Z;
           end = min(T, pos + Z);
           c = locate(pos);
@@ -419,15 +414,42 @@ __global__ void __launch_bounds__(THREADS, 1)
         while (off[c + 1] <= pos) ++c;
         const int tw = (off[c + 1] - off[c]) / spr;
         const int rel = pos - off[c];
-        r = rel / tw;
-        const int u0 = rel - r * tw, u1 = min(tw, u0 + (end - pos));
+        q.r = rel / tw;
+        const int u0 = rel - q.r * tw, u1 = min(tw, u0 + (end - pos));
         pos += u1 - u0;
-        lt0 = max(u0 - kAttn8SeqUnits, 0);
-        n_tiles = max(u1 - kAttn8SeqUnits - lt0, 0);
+        q.lt0 = max(u0 - kAttn8SeqUnits, 0);
+        q.n = max(u1 - kAttn8SeqUnits - q.lt0, 0);
       }
-      if (done) break;
-      const int g = r % Hkv, rb = r / Hkv;
-      const int ctx = a.ctx_lens[c];
+      q.c = c, q.k = k, q.ctx = a.ctx_lens[c];
+      return q;
+    };
+    const int pshift = (page & (page - 1)) == 0 ? __ffs(page) - 1 : -1;
+    auto page_index = [&](int t) -> int { return pshift >= 0 ? t >> pshift : t / page; };
+    // Page ids: one load brings the ids of a window of four tiles (at most 32 pages of 16 or
+    // more keys), one per lane, a window ahead of its use; the index is clamped into the
+    // request's row of the table (ids past the context's end are never used).
+    auto window = [&](const Piece& q, int w) -> int {
+      const int idx = page_index((q.lt0 + 4 * w) * TT) + lane;
+      return a.kv.table[(size_t)q.c * a.kv.max_pages + min(idx, a.kv.max_pages - 1)];
+    };
+    int tile_i = 0;   // tiles this warp has armed (its arrival on their stage)
+    int s = 0, s_par = 1;  // the tile's stage and the parity to wait for
+    int q_last = -1;  // warp 0: the last piece whose queries it armed
+    bool ok = true;
+    // Every producer warp walks the same pieces and passes the same barriers: the loop
+    // ends only at one, when the work is done or a producer has given up waiting.
+    bool stopped = false;
+    Piece next = advance();
+    int next_ids = next.n > 0 ? window(next, 0) : 0;
+    for (int seq = 0;; ++seq) {
+      if (tc::bar_or<1, 32 * NPW>(!ok)) {
+        stopped = true;
+        break;
+      }
+      const Piece pc = next;
+      if (pc.n == 0) break;
+      const int g = pc.r % Hkv, rb = pc.r / Hkv;
+      const int ctx = pc.ctx, n_tiles = pc.n;
       const int ct = (ctx + TT - 1) / TT;  // context tiles of the sequence
       const int qslot = seq % L::NQ, quse = seq / L::NQ;
 
@@ -438,37 +460,30 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (ok) {
             q_last = seq;
             tc::mbar_arrive_expect_tx(&ms.q_full[qslot], (uint32_t)L::Q_BYTES);
-            tc::bulk_load(sQ + qslot * L::Q_BUF, a.q_img + ((size_t)c * spr + r) * L::Q_BYTES, (uint32_t)L::Q_BYTES,
-                          &ms.q_full[qslot]);
+            tc::bulk_load(sQ + qslot * L::Q_BUF, a.q_img + ((size_t)pc.c * spr + pc.r) * L::Q_BYTES,
+                          (uint32_t)L::Q_BYTES, &ms.q_full[qslot]);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         q_last = __shfl_sync(0xffffffffu, q_last, 0);
       }
 
-      // Page ids of the lane's keys are read three tiles ahead (the table index clamped into
-      // the request's row: ids past the context's end are never used).  The scales are
-      // four-byte asynchronous copies into the stage that the stage's barrier waits for, so
-      // their latency runs beside the pages' own.
-      const int32_t* table = a.kv.table + (size_t)c * a.kv.max_pages;
-      auto page_of = [&](int local) -> int {
-        const int idx = ((lt0 + local) * TT + sub) / page;
-        return table[idx < a.kv.max_pages ? idx : a.kv.max_pages - 1];
-      };
-      int pid0 = page_of(0), pid1 = page_of(1), pid2 = page_of(2);
-
-      for (int local = 0; local < n_tiles && ok; ++local, ++tile_i) {
-        const int pid = pid0;
-        pid0 = pid1, pid1 = pid2;
-        pid2 = page_of(local + 3);
-        const int s = tile_i % NS;
-        ok = tc::mbar_wait_warp(&ms.kv_empty[s], ((tile_i / NS) & 1) ^ 1, err, lim);
+      int ids = next_ids, ids_ahead = n_tiles > 4 ? window(pc, 1) : 0, base = page_index(pc.lt0 * TT);
+      for (int local = 0; local < n_tiles && ok; ++local) {
+        if (local > 0 && (local & 3) == 0) {
+          ids = ids_ahead;
+          base = page_index((pc.lt0 + local) * TT);
+          if (local + 4 < n_tiles) ids_ahead = window(pc, local / 4 + 1);
+        }
+        const int st = pc.lt0 + local;  // tile of the sequence
+        const int t0 = st * TT;
+        const int pidx = page_index(t0 + sub);
+        const int pid = __shfl_sync(0xffffffffu, ids, (pidx - base) & 31);
+        ok = tc::mbar_wait_warp(&ms.kv_empty[s], s_par, err, lim);
         if (!ok) break;
         uint8_t* kd = sKV + s * L::STAGE;
         uint8_t* vd = kd + L::KV;
-        const int st = lt0 + local;  // tile of the sequence
         const bool block = st >= ct;
-        const int t0 = st * TT;
         const int valid = block ? a.K : min(TT, ctx - t0);
         if (has_scale) {
           float* to = &ms.scale[s][(is_v ? 8 : 0) + grp];
@@ -488,7 +503,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     (local >= n_tiles - STEP ? kGroupLast : 0) | (block ? kBlock : 0) |
                     (joff + valid - 1 > 0 ? kMixed : 0) | (quse & 1 ? kQPar : 0) | (qslot ? kQSlot : 0) |
                     (local & 1 ? kHalf : 0);
-          m.cg = c * Hkv + g, m.rb = rb, m.slot = c * spr + r + k, m.valid = valid, m.joff = joff;
+          m.cg = pc.c * Hkv + g, m.rb = rb, m.slot = pc.c * spr + pc.r + pc.k, m.valid = valid, m.joff = joff;
           m.pad[0] = m.pad[1] = 0;
           ms.meta[s] = m;
           ms.v_nan[s] = make_uint4(0, 0, 0, 0);
@@ -497,9 +512,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           // the block's K (warp 0) and V (warp 1) images: hi rows, then lo rows
           const uint32_t bytes = (uint32_t)(2 * blk_rows(a.K) * D);
           if (lane == 0) {
-            if (pw < 2) {
+            if (pw < 2) {  // (NPW >= 2)
               tc::mbar_arrive_expect_tx(&ms.kv_full[s], bytes);
-              tc::bulk_load(pw == 0 ? kd : vd, a.blk_img + ((size_t)(c * Hkv + g) * 2 + pw) * bytes, bytes,
+              tc::bulk_load(pw == 0 ? kd : vd, a.blk_img + ((size_t)(pc.c * Hkv + g) * 2 + pw) * bytes, bytes,
                             &ms.kv_full[s]);
             } else {
               tc::mbar_arrive(&ms.kv_full[s]);
@@ -517,10 +532,16 @@ __global__ void __launch_bounds__(THREADS, 1)
               pg = 0;  // keep the copy in bounds (its scales are 0 here)
             }
             tc::tma_load_3d_hint((is_v ? vd : kd) + sub * D, is_v ? &maps.v : &maps.k, &ms.kv_full[s], 0,
-                                 (t0 + sub) % page, pg * Hkv + g, once);
+                                 t0 + sub - pidx * page, pg * Hkv + g, once);
           }
         }
         __syncwarp();
+        ++tile_i;
+        if (++s == NS) s = 0, s_par ^= 1;
+        if (local == 0) {  // look ahead while the ring is full
+          next = advance();
+          next_ids = next.n > 0 ? window(next, 0) : 0;
+        }
       }
     }
     // No copy may land after the CTA has finished: wait, with the full limit, for the last
@@ -535,8 +556,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
     // sentinel stage: no more work
     if (!stopped) {
-      const int s = tile_i % NS;
-      if (tc::mbar_wait_warp(&ms.kv_empty[s], ((tile_i / NS) & 1) ^ 1, err, lim) && (lane == 0 || has_scale)) {
+      if (tc::mbar_wait_warp(&ms.kv_empty[s], s_par, err, lim) && (lane == 0 || has_scale)) {
         if (threadIdx.x == 0) ms.meta[s].flags = kEnd;
         tc::mbar_arrive(&ms.kv_full[s]);
       }
@@ -656,19 +676,25 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
     // ------------------------------------------------------------ softmax groups
-    // The thread's key is its lane of the tile; it holds all NR columns of its group's item.
-    // A wait that gave up (ok = false) is acted on only at the group's barriers, so that
-    // all four warps leave together.
-    const int w = (warp - SM_WARP0) >> 2, quarter = warp & 3;
+    // Groups 2 w and 2 w + 1 take the two halves of the columns of the items of side w.  The
+    // thread's key is its lane of the tile.  A wait that gave up (ok = false) is acted on only
+    // at the group's barriers, so that all four warps leave together.
+    const int gq = (warp - SM_WARP0) >> 2, w = gq >> 1, quarter = warp & 3;
+    const int c0 = (gq & 1) * NC;  // first column
     const int key = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t t_hi = tmem + lane_off + L::O_COL(w), t_lo = t_hi + PN / 2;
-    float2* col = ms.col[w];
-    float* alpha = ms.alpha[w];
+    const uint32_t t_hi = tmem + lane_off + L::O_COL(w) + c0, t_lo = t_hi + PN / 2;
+    float2* col = ms.col[gq];
+    float* alpha = ms.alpha[gq];
     auto group_or = [&](bool p) -> bool {
-      return w == 0 ? tc::bar_or<2, 128>(p) : tc::bar_or<3, 128>(p);
+      switch (gq) {
+        case 0: return tc::bar_or<2, 128>(p);
+        case 1: return tc::bar_or<3, 128>(p);
+        case 2: return tc::bar_or<4, 128>(p);
+        default: return tc::bar_or<5, 128>(p);
+      }
     };
-    float l[NR];        // this key lane's share of the columns' sums
+    float l[NC];        // this key lane's share of the columns' sums
     float Mv = 0.f, inv_mv = 0.f;  // largest V scale of the piece, 1 / it
     bool ok = true;
     // the previous piece's partial, still in O^T
@@ -681,32 +707,37 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc::tc_fence_after();
       const int d = D == 128 ? key : quarter * 16 + lane;
       const bool on = D == 128 || lane < 16;
-#pragma unroll
-      for (int j0 = 0; j0 < NR; j0 += 16) {
-        float hi[16], lo[16];
+#pragma unroll 1
+      for (int j0 = 0; j0 < NC; j0 += 8) {
+        float hi[8], lo[8];
         tc::tmem_ld(t_hi + j0, hi);
         tc::tmem_ld(t_lo + j0, lo);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < 8; ++j)
           if (on && j0 + j < pend_rows)
             a.ws_acc[(pend_base + j0 + j) * D + d] = fmaf(lo[j], 1.f / kLoScale, hi[j]) * pend_mul;
       }
       pend = false;
     };
 
-    int n = 0;  // items of the group so far
+    int n = 0;  // items of the side so far
+    int s = PAIR ? 0 : w;  // the item's stage
     for (;; ++n) {
-      const int it = 2 * n + w, b = it & 3, s = (PAIR ? n : it) % NS;
+      const int it = 2 * n + w, b = it & 3;
       if (ok) ok = wait(&ms.s_full[b], (it >> 2) & 1);
       const bool run = ok && it < *(volatile int*)&ms.end_item;
       TileMeta m = {};
       int cmin = 0;
       bool first = false;
-      const float* cq_first = nullptr;
-      float e[NR], sv = 0.f;
+      float e[NC], sv = 0.f;
       float e_max = -INFINITY;
       if (run) {
+        tc::tc_fence_after();
         m = load_meta(&ms.meta[s]);
+        ld_columns<NC>(tmem + lane_off + L::S_COL(b) + c0, e);
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ms.s_free[b]);
         first = (m.flags & kGroupFirst) != 0;
         float ck = 0.f;
         if (key < m.valid) {
@@ -719,20 +750,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         ck *= scale_log2;
         // columns below cmin do not see this key (row = rb ROWS + column, position row / G)
-        cmin = key >= m.valid ? NR : max(m.joff + key, 0) * G - m.rb * L::ROWS - (PAIR ? w * NR : 0);
-        tc::tc_fence_after();
-        ld_columns<NR>(tmem + lane_off + L::S_COL(b), e);
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ms.s_free[b]);
-        const float2 ck2 = make_float2(ck, ck);
+        cmin = key >= m.valid ? NC : max(m.joff + key, 0) * G - m.rb * L::ROWS - (PAIR ? w * NR : 0) - c0;
         if (first) {
-          cq_first = (const float*)(sQ + (m.flags & kQSlot ? L::Q_BUF : 0) + 2 * L::ROWS * D) + (PAIR ? w * NR : 0);
+          // the queries' scales, and no maximum yet (each warp writes the same for itself)
+          const float* cq = (const float*)(sQ + (m.flags & kQSlot ? L::Q_BUF : 0) + 2 * L::ROWS * D) +
+                            (PAIR ? w * NR : 0) + c0;
 #pragma unroll
-          for (int j = 0; j < NR; ++j) e[j] *= ck * cq_first[j];
+          for (int j = 0; j < NC; ++j) e[j] *= ck * cq[j];
         } else {
+          const float2 ck2 = make_float2(ck, ck);
 #pragma unroll
-          for (int j = 0; j < NR; j += 2) {
+          for (int j = 0; j < NC; j += 2) {
             const float4 cm = *(const float4*)&col[j];
             const float2 x = tc::ffma2(tc::fmul2(make_float2(e[j], e[j + 1]), ck2), make_float2(cm.x, cm.z),
                                        make_float2(cm.y, cm.w));
@@ -741,12 +769,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (cmin > 0) {
 #pragma unroll
-          for (int j = 0; j < NR; ++j)
+          for (int j = 0; j < NC; ++j)
             if (j < cmin) e[j] = -INFINITY;
         }
         float mx[4] = {e[0], e[1], e[2], e[3]};
 #pragma unroll
-        for (int j = 4; j < NR; j += 4)
+        for (int j = 4; j < NC; j += 4)
 #pragma unroll
           for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], e[j + k]);
         e_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
@@ -755,26 +783,28 @@ __global__ void __launch_bounds__(THREADS, 1)
         // The maxima move (or the group leaves).  s = e + m (e alone in a first tile).
         if (run) {
 #pragma unroll
-          for (int j = 0; j < NR; ++j) {
+          for (int j = 0; j < NC; ++j) {
             if (!first) e[j] -= col[j].y;
             const int top = __reduce_max_sync(0xffffffffu, float_key(e[j]));
-            if (lane == (j & 31)) ms.cmax[w][quarter][j] = key_float(top);
+            if (lane == j) ms.cmax[gq][quarter][j] = key_float(top);
           }
           const float t = warp_max(sv);
-          if (lane == 0) ms.svmax[w][quarter] = t;
+          if (lane == 0) ms.svmax[gq][quarter] = t;
         }
         if (group_or(!run)) break;
-        if (quarter == 0) {
-          for (int j = lane; j < NR; j += 32) {
-            const float cm = fmaxf(fmaxf(ms.cmax[w][0][j], ms.cmax[w][1][j]), fmaxf(ms.cmax[w][2][j], ms.cmax[w][3][j]));
-            const float m_old = first ? -INFINITY : ms.m[w][j], m_new = fmaxf(m_old, cm);
-            const float cq = first ? cq_first[j] : col[j].x;
-            ms.m[w][j] = m_new;
-            col[j] = make_float2(cq, m_new == -INFINITY ? 0.f : -m_new);
-            alpha[j] = m_old == -INFINITY ? 1.f : exp2f(m_old - m_new);
-          }
+        if (quarter == 0 && lane < NC) {
+          const int j = lane;
+          const float cm =
+              fmaxf(fmaxf(ms.cmax[gq][0][j], ms.cmax[gq][1][j]), fmaxf(ms.cmax[gq][2][j], ms.cmax[gq][3][j]));
+          const float m_old = first ? -INFINITY : ms.m[gq][j], m_new = fmaxf(m_old, cm);
+          const float cq = first ? ((const float*)(sQ + (m.flags & kQSlot ? L::Q_BUF : 0) + 2 * L::ROWS * D))
+                                       [(PAIR ? w * NR : 0) + c0 + j]
+                                 : col[j].x;
+          ms.m[gq][j] = m_new;
+          col[j] = make_float2(cq, m_new == -INFINITY ? 0.f : -m_new);
+          alpha[j] = m_old == -INFINITY ? 1.f : exp2f(m_old - m_new);
         }
-        const float sv_top = fmaxf(fmaxf(ms.svmax[w][0], ms.svmax[w][1]), fmaxf(ms.svmax[w][2], ms.svmax[w][3]));
+        const float sv_top = fmaxf(fmaxf(ms.svmax[gq][0], ms.svmax[gq][1]), fmaxf(ms.svmax[gq][2], ms.svmax[gq][3]));
         const float mv_new = first ? sv_top : fmaxf(Mv, sv_top);
         const float mv_ratio = mv_new > 0.f ? Mv / mv_new : 0.f;
         Mv = mv_new;
@@ -782,32 +812,34 @@ __global__ void __launch_bounds__(THREADS, 1)
         group_or(false);  // col, m and alpha are written
         if (first) {
 #pragma unroll
-          for (int j = 0; j < NR; ++j) l[j] = 0.f;
+          for (int j = 0; j < NC; ++j) l[j] = 0.f;
         } else {
 #pragma unroll
-          for (int j = 0; j < NR; ++j) l[j] *= alpha[j];
-          // O^T holds the group's earlier tiles of the piece once its last product is done
+          for (int j = 0; j < NC; ++j) l[j] *= alpha[j];
+          // O^T holds the side's earlier tiles of the piece once its last product is done
           ok = wait(&ms.pv_done[w], (n - 1) & 1);
           if (ok) {
             tc::tc_fence_after();
+#pragma unroll 1
+            for (int j0 = 0; j0 < NC; j0 += 8) {
+              float o[8], p[8];
+              tc::tmem_ld(t_hi + j0, o);
+              tc::tmem_ld(t_lo + j0, p);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int j0 = 0; j0 < NR; j0 += 8) {
-                float o[8];
-                const uint32_t t = (h ? t_lo : t_hi) + j0;
-                tc::tmem_ld(t, o);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] *= alpha[j0 + j] * mv_ratio;
-                tc::tmem_st8(t, o);
+              for (int j = 0; j < 8; ++j) {
+                const float f = alpha[j0 + j] * mv_ratio;
+                o[j] *= f, p[j] *= f;
               }
+              tc::tmem_st8(t_hi + j0, o);
+              tc::tmem_st8(t_lo + j0, p);
+            }
           }
         }
 #pragma unroll
-        for (int j = 0; j < NR; ++j) e[j] += col[j].y;
+        for (int j = 0; j < NC; ++j) e[j] += col[j].y;
       }
       // From here on a failed wait only skips work; the group leaves at the next barrier.
-      // The group's last product is done: its P buffer is free, and O^T is complete if the
+      // The side's last product is done: its P buffer is free, and O^T is complete if the
       // previous piece's partial is still to be written (before this item's product may
       // overwrite it).
       if (ok && n > 0) ok = wait(&ms.pv_done[w], (n - 1) & 1);
@@ -816,8 +848,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (m.flags & kMixed) {
         // a NaN in a V row that some column does not see: the product would carry it into
         // that column, too, so the row is cleared and the columns that see it get a NaN sum.
-        // PAIR: the other group may have cleared the row already, and has then marked it
-        // before.
+        // Another group may have cleared the row already, and has then marked it before.
         bool bad = false;
         if (key < m.valid)
           for (int h = 0; h < (m.flags & kBlock ? 2 : 1); ++h)
@@ -827,34 +858,33 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
               for (int z = 0; z < 4; ++z) bad = bad || __vcmpeq4(xs[z] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
             }
-        if constexpr (PAIR) {
-          volatile uint32_t* mark = &ms.v_nan[s].x + quarter;
-          if (bad) atomicOr((uint32_t*)mark, 1u << lane);
-          __threadfence_block();
-          bad = bad || (*mark >> lane & 1) != 0;
-        }
+        volatile uint32_t* mark = &ms.v_nan[s].x + quarter;
+        if (bad) atomicOr((uint32_t*)mark, 1u << lane);
+        __threadfence_block();
+        bad = bad || (*mark >> lane & 1) != 0;
         if (bad) {
           for (int h = 0; h < (m.flags & kBlock ? 2 : 1); ++h)
             for (int q = 0; q < D / 16; ++q)
               *(uint4*)(v_row + h * blk_rows(a.K) * D + q * 16) = make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int j = 0; j < NR; ++j)
+          for (int j = 0; j < NC; ++j)
             if (j >= cmin) l[j] = __int_as_float(0x7fffffff);
         }
       }
       // V rows past the last key may hold anything (their weights are 0): clear them
       if (!(m.flags & kBlock) && key >= m.valid && key < ((m.valid + 31) & ~31)) {
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < D / 16; ++q) *(uint4*)(v_row + q * 16) = make_uint4(0, 0, 0, 0);
       }
       const float rv = sv * inv_mv * kPScale;
       const float2 rv2 = make_float2(rv, rv);
       uint8_t* prow = sP + w * L::P_BUF + key * 128;
+      constexpr int CH = NC % 16 == 0 ? 16 : 8;
 #pragma unroll
-      for (int j0 = 0; j0 < NR; j0 += 16) {
-        uint32_t hi[4], lo[4];
+      for (int j0 = 0; j0 < NC; j0 += CH) {
+        uint32_t hi[CH / 4], lo[CH / 4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < CH / 4; ++q) {
           uint32_t hh[2], ll[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -872,9 +902,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           hi[q] = hh[0] | (hh[1] << 16);
           lo[q] = ll[0] | (ll[1] << 16);
         }
+        // byte c0 + j0 of the row's high half, and of its low half 64 bytes on
+        const int ch = (c0 + j0) / 16;
         if (ok) {
-          *(uint4*)(prow + (((j0 / 16) ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *(uint4*)(prow + (((4 + j0 / 16) ^ (key & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if constexpr (CH == 16) {
+            *(uint4*)(prow + ((ch ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *(uint4*)(prow + (((4 + ch) ^ (key & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else {
+            const int in = (c0 + j0) & 8;
+            *(uint2*)(prow + ((ch ^ (key & 7)) << 4) + in) = make_uint2(hi[0], hi[1]);
+            *(uint2*)(prow + (((4 + ch) ^ (key & 7)) << 4) + in) = make_uint2(lo[0], lo[1]);
+          }
         }
       }
       tc::fence_proxy_async();
@@ -883,28 +921,28 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (ok && lane == 0) tc::mbar_arrive(&ms.p_full[w]);
 
       if (m.flags & kGroupLast) {
-        // the group's part of the piece is complete: its sums now, its O^T during the next
+        // the side's part of the piece is complete: its sums now, its O^T during the next
         // item
-        const int rows = min(NR, min(L::ROWS, R - m.rb * L::ROWS) - (PAIR ? w * NR : 0));
+        const int rows = min(NC, min(L::ROWS, R - m.rb * L::ROWS) - (PAIR ? w * NR : 0) - c0);
         const size_t base =
-            PAIR ? (size_t)m.slot * RB + w * NR : ((size_t)m.slot * 2 + (m.flags & kHalf ? 1 : 0)) * RB;
+            (PAIR ? (size_t)m.slot * RB + w * NR : ((size_t)m.slot * 2 + (m.flags & kHalf ? 1 : 0)) * RB) + c0;
 #pragma unroll
-        for (int j = 0; j < NR; ++j) {
+        for (int j = 0; j < NC; ++j) {
           const float t = warp_sum(l[j]);
-          if (lane == (j & 31)) ms.cmax[w][quarter][j] = t;
+          if (lane == j) ms.cmax[gq][quarter][j] = t;
         }
         group_or(false);
-        if (quarter == 0) {
-          for (int j = lane; j < rows; j += 32) {
-            float* ml = a.ws_ml + (base + j) * 2;
-            ml[0] = ms.m[w][j];
-            ml[1] = (ms.cmax[w][0][j] + ms.cmax[w][1][j]) + (ms.cmax[w][2][j] + ms.cmax[w][3][j]);
-          }
+        if (quarter == 0 && lane < rows) {
+          float* ml = a.ws_ml + (base + lane) * 2;
+          ml[0] = ms.m[gq][lane];
+          ml[1] = (ms.cmax[gq][0][lane] + ms.cmax[gq][1][lane]) + (ms.cmax[gq][2][lane] + ms.cmax[gq][3][lane]);
         }
         group_or(false);  // cmax and m may be written again
         pend = true, pend_base = base, pend_rows = rows;
         pend_mul = Mv * (1.f / kPScale);
       }
+      s += PAIR ? 1 : 2;
+      if (s >= NS) s -= NS;
     }
     if (ok && pend && wait(&ms.pv_done[w], (n - 1) & 1)) write_partial();  // the last piece's
     tc::tc_fence_before();
