@@ -52,10 +52,10 @@ constexpr int NPW = 2;          // producer warps
 constexpr int SM_WARP0 = 4;     // first softmax warp (a multiple of 4: warp % 4 is its TMEM quarter)
 constexpr int SMW = 16;         // softmax warps: four groups of four
 constexpr int THREADS = 32 * (SM_WARP0 + SMW);
-// registers per thread after the launch's 96: 128 * 56 + 512 * 104 <= 640 * 96
-constexpr int kFewRegs = 56, kManyRegs = 104;
-constexpr float kPScale = 32.f;   // 2^5: weights enter P times this
-constexpr float kMaxExp = 3.f;    // a weight's exponent may reach this before the maximum moves
+// registers per thread after the launch's 96: 128 * 64 + 512 * 104 = 640 * 96
+constexpr int kFewRegs = 64, kManyRegs = 104;
+constexpr float kPScale = 8.f;    // 2^3: weights enter P times this
+constexpr float kMaxExp = 5.f;    // a weight's exponent may reach this before the maximum moves
 constexpr float kLoScale = 16.f;  // the low part of P is held times this
 constexpr int kMaxChunksAuto = 256, kMaxChunksExplicit = 2048;
 constexpr int kBlkRows = 64;      // scales of a block's rows (K <= 64)
@@ -122,7 +122,8 @@ struct Misc {
   TileMeta meta[8];
   float scale[8][16];       // per stage: K scales of its eight 16-key groups, then V scales
   // per softmax group
-  alignas(16) float2 col[4][NR / 2];  // (query row's scale, -maximum)
+  alignas(16) float cq[4][NR / 2];    // the query rows' scales
+  alignas(16) float nm[4][NR / 2];    // -maximum (0 while there is none)
   alignas(16) float alpha[4][NR / 2];
   float m[4][NR / 2];
   float cmax[4][4][NR / 2]; // per warp: column maxima, later the rows' sums
@@ -263,6 +264,27 @@ __device__ __forceinline__ int float_key(float v) {
 }
 __device__ __forceinline__ float key_float(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 
+// Four weights (fp16: 11 bits, well below the two parts' error) as their e4m3 codes and the
+// codes of what those leave, times kLoScale.
+__device__ __forceinline__ void split_weights(__half2 p0, __half2 p1, uint32_t& hi, uint32_t& lo) {
+  asm("{\n\t.reg .b16 a, b, c, d;\n\t.reg .b32 x, y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 b, %3;\n\t"
+      "mov.b32 %0, {a, b};\n\t"
+      "cvt.rn.f16x2.e4m3x2 x, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 y, b;\n\t"
+      "sub.rn.f16x2 x, %2, x;\n\t"
+      "sub.rn.f16x2 y, %3, y;\n\t"
+      "mul.rn.f16x2 x, x, %4;\n\t"
+      "mul.rn.f16x2 y, y, %4;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 c, x;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 d, y;\n\t"
+      "mov.b32 %1, {c, d};\n\t}\n"
+      : "=&r"(hi), "=&r"(lo)
+      : "r"(*reinterpret_cast<uint32_t*>(&p0)), "r"(*reinterpret_cast<uint32_t*>(&p1)), "r"(0x4C004C00u));
+}
+static_assert(kLoScale == 16.f, "0x4C00 is 16 in fp16");
+
 // One lane of a converged warp (the tensor instructions are issued by it).
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -285,29 +307,13 @@ __device__ __forceinline__ TileMeta load_meta(const TileMeta* m) {
   return r;
 }
 
-// N consecutive columns of this thread's TMEM lane.
-template <int N>
-__device__ __forceinline__ void ld_columns(uint32_t at, float (&e)[N]) {
-  if constexpr (N == 24) {
-    float a[16], b[8];
-    tc::tmem_ld(at, a);
-    tc::tmem_ld(at + 16, b);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) e[j] = a[j];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e[16 + j] = b[j];
-  } else {
-    tc::tmem_ld(at, e);
-  }
-}
-
 // An item is one tile's work for one softmax group: item 2 n + w is the n-th of group w.
 // PAIR = false (up to 64 query rows a sequence): the groups take the tiles in turn, item
 // = tile.  PAIR = true (up to 128 rows): each takes one half of the rows of every tile,
 // tile = item / 2, so that a tile's bytes serve both halves.
 template <int D, int NR, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
-    attn_kv8_tc_kernel(const __grid_constant__ Maps maps, const AttnKv8Args a, float scale_log2, int box_rows) {
+    attn_kv8_tc_kernel(const __grid_constant__ Maps maps, const AttnKv8Args a, float scale_log2, int box_shift) {
   using L = Lay<D, NR, PAIR>;
   constexpr int NS = L::NS, PN = L::PN, NC = NR / 2;
   extern __shared__ uint8_t smem_raw[];
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint64_t lim = a.wait_ns ? (uint64_t)a.wait_ns : tc::kWaitLimitNs;  // pipeline waits
   constexpr int QK_WARP = NPW, PV_WARP = NPW + 1;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // for a whole warp
-    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, err, lim));
+    return __all_sync(0xffffffffu, tc::mbar_wait_long(bar, parity, err, lim));
   };
 
   if (threadIdx.x == 0) {
@@ -360,19 +366,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp < NPW) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     // ------------------------------------------------------------ producers
-    // Box bx < nb is rows [bx box_rows, ...) of K, box nb + bx of V, issued by lane
-    // bx / NPW of warp bx % NPW.  SL lanes from 16 on bring the scales of 16-key groups, half
-    // of them K's.  All producer warps walk the same tiles; warp 0 loads the queries and
-    // describes the tile.
-    const int pw = warp, nb = TT / box_rows;
-    const int bx = pw + NPW * lane;
-    constexpr int SL = 16 / NPW;
-    const bool has_box = lane < 16 && bx < 2 * nb;
-    const bool has_scale = lane >= 16 && lane < 16 + SL;
-    const int grp = pw * (SL / 2) + (lane & (SL / 2 - 1));
-    const bool is_v = has_scale ? (lane & (SL / 2)) != 0 : bx >= nb;
-    const int sub = has_scale ? 16 * grp : (bx % nb) * box_rows;  // first key of the tile that concerns the lane
-    const float* scales = is_v ? a.kv.vs : a.kv.ks;
+    // Warp 0 brings K, warp 1 V: lane x < 8 the tile's box x of 2^box_shift rows (within one
+    // page each), lane 8 + i the scale of its 16-key group i.  Both walk the same tiles;
+    // warp 0 also loads the queries and describes the tile.  (One warp's instructions from
+    // tile to tile bound the whole kernel when R is small: the loop is kept short.)
+    const int pw = warp;
+    const int sub = lane < 8 ? lane << box_shift : 16 * (lane & 7);  // first key of the tile that concerns the lane
+    const CUtensorMap* map = pw == 1 ? &maps.v : &maps.k;
+    const float* scales = pw == 1 ? a.kv.vs : a.kv.ks;
+    const uint32_t scale_at = tc::smem_u32(&ms.scale[0][8 * pw + (lane & 7)]);
     if (threadIdx.x == 0) {
       tc::tma_prefetch_desc(&maps.k);
       tc::tma_prefetch_desc(&maps.v);
@@ -477,23 +479,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         const int st = pc.lt0 + local;  // tile of the sequence
         const int t0 = st * TT;
-        const int pidx = page_index(t0 + sub);
-        const int pid = __shfl_sync(0xffffffffu, ids, (pidx - base) & 31);
-        ok = tc::mbar_wait_warp(&ms.kv_empty[s], s_par, err, lim);
-        if (!ok) break;
-        uint8_t* kd = sKV + s * L::STAGE;
-        uint8_t* vd = kd + L::KV;
         const bool block = st >= ct;
         const int valid = block ? a.K : min(TT, ctx - t0);
-        if (has_scale) {
-          float* to = &ms.scale[s][(is_v ? 8 : 0) + grp];
-          if (block || sub >= valid || pid < 0 || pid >= a.kv.num_pages) {
-            *to = 0.f;
-            tc::mbar_arrive(&ms.kv_full[s]);
-          } else {
-            tc::cp_async4(to, scales + (size_t)pid * Hkv + g);
-            tc::cp_async_arrive(&ms.kv_full[s]);
-          }
+        const int tk = t0 + sub, pidx = page_index(tk);
+        int pid = __shfl_sync(0xffffffffu, ids, (pidx - base) & 31);
+        const bool in = !block && sub < valid && lane < 16;
+        const bool sound = (unsigned)pid < (unsigned)a.kv.num_pages;
+        if (in && !sound) flag_error(err, kErrPageOOB);
+        if (!sound) pid = 0;  // keep the copy in bounds (its scales are 0 here)
+        const int row = pid * Hkv + g;
+        ok = tc::mbar_wait_warp(&ms.kv_empty[s], s_par, err, lim);
+        if (!ok) break;
+        uint8_t* dst = sKV + s * L::STAGE + pw * L::KV;
+        if (lane >= 8 && lane < 16) {
+          tc::cp_async4(scale_at + s * 64, scales + row, in && sound);
+          tc::cp_async_arrive(&ms.kv_full[s]);
         }
         if (pw == 0 && lane == 0) {
           const int joff = !a.causal ? -TT : block ? 0 : a.kb ? -TT : max(t0 - ctx + a.K, -TT);
@@ -506,34 +506,21 @@ __global__ void __launch_bounds__(THREADS, 1)
           m.cg = pc.c * Hkv + g, m.rb = rb, m.slot = pc.c * spr + pc.r + pc.k, m.valid = valid, m.joff = joff;
           m.pad[0] = m.pad[1] = 0;
           ms.meta[s] = m;
-          ms.v_nan[s] = make_uint4(0, 0, 0, 0);
+          if (m.flags & kMixed) ms.v_nan[s] = make_uint4(0, 0, 0, 0);
         }
         if (block) {
-          // the block's K (warp 0) and V (warp 1) images: hi rows, then lo rows
+          // the block's K or V image: hi rows, then lo rows
           const uint32_t bytes = (uint32_t)(2 * blk_rows(a.K) * D);
           if (lane == 0) {
-            if (pw < 2) {  // (NPW >= 2)
-              tc::mbar_arrive_expect_tx(&ms.kv_full[s], bytes);
-              tc::bulk_load(pw == 0 ? kd : vd, a.blk_img + ((size_t)(pc.c * Hkv + g) * 2 + pw) * bytes, bytes,
-                            &ms.kv_full[s]);
-            } else {
-              tc::mbar_arrive(&ms.kv_full[s]);
-            }
+            tc::mbar_arrive_expect_tx(&ms.kv_full[s], bytes);
+            tc::bulk_load(dst, a.blk_img + ((size_t)(pc.c * Hkv + g) * 2 + pw) * bytes, bytes, &ms.kv_full[s]);
           }
         } else {
-          const bool mine = has_box && sub < valid;
-          const uint32_t warp_bytes = __reduce_add_sync(0xffffffffu, mine ? (uint32_t)(box_rows * D) : 0u);
-          if (lane == 0) tc::mbar_arrive_expect_tx(&ms.kv_full[s], warp_bytes);  // also this warp's arrival
+          const int boxes = (valid + (1 << box_shift) - 1) >> box_shift;
+          if (lane == 0) tc::mbar_arrive_expect_tx(&ms.kv_full[s], (uint32_t)((boxes << box_shift) * D));
           __syncwarp();
-          if (mine) {
-            int pg = pid;
-            if (pg < 0 || pg >= a.kv.num_pages) {
-              flag_error(err, kErrPageOOB);
-              pg = 0;  // keep the copy in bounds (its scales are 0 here)
-            }
-            tc::tma_load_3d_hint((is_v ? vd : kd) + sub * D, is_v ? &maps.v : &maps.k, &ms.kv_full[s], 0,
-                                 t0 + sub - pidx * page, pg * Hkv + g, once);
-          }
+          if (lane < boxes)
+            tc::tma_load_3d_hint(dst + sub * D, map, &ms.kv_full[s], 0, tk - pidx * page, row, once);
         }
         __syncwarp();
         ++tile_i;
@@ -556,7 +543,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
     // sentinel stage: no more work
     if (!stopped) {
-      if (tc::mbar_wait_warp(&ms.kv_empty[s], s_par, err, lim) && (lane == 0 || has_scale)) {
+      if (tc::mbar_wait_warp(&ms.kv_empty[s], s_par, err, lim) && lane < 9) {  // as many arrivals as a tile's
         if (threadIdx.x == 0) ms.meta[s].flags = kEnd;
         tc::mbar_arrive(&ms.kv_full[s]);
       }
@@ -684,17 +671,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int key = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t t_hi = tmem + lane_off + L::O_COL(w) + c0, t_lo = t_hi + PN / 2;
-    float2* col = ms.col[gq];
+    float *cqs = ms.cq[gq], *nms = ms.nm[gq];
     float* alpha = ms.alpha[gq];
-    auto group_or = [&](bool p) -> bool {
-      switch (gq) {
-        case 0: return tc::bar_or<2, 128>(p);
-        case 1: return tc::bar_or<3, 128>(p);
-        case 2: return tc::bar_or<4, 128>(p);
-        default: return tc::bar_or<5, 128>(p);
-      }
-    };
-    float l[NC];        // this key lane's share of the columns' sums
+    auto group_or = [&](bool p) -> bool { return tc::bar_or(2 + gq, 128, p); };
+    constexpr int CH = NC % 16 == 0 ? 16 : 8;  // columns at a time
+    tc::F2 l2[NC / 2];  // this key lane's share of the columns' sums
     float Mv = 0.f, inv_mv = 0.f;  // largest V scale of the piece, 1 / it
     bool ok = true;
     // the previous piece's partial, still in O^T
@@ -729,17 +710,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       TileMeta m = {};
       int cmin = 0;
       bool first = false;
-      float e[NC], sv = 0.f;
+      float ck = 0.f, sv = 0.f;
       float e_max = -INFINITY;
+      const uint32_t t_s = tmem + lane_off + L::S_COL(b) + c0;
       if (run) {
         tc::tc_fence_after();
         m = load_meta(&ms.meta[s]);
-        ld_columns<NC>(tmem + lane_off + L::S_COL(b) + c0, e);
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ms.s_free[b]);
         first = (m.flags & kGroupFirst) != 0;
-        float ck = 0.f;
         if (key < m.valid) {
           if (m.flags & kBlock) {
             const float* bs = a.blk_scale + (size_t)m.cg * 2 * kBlkRows;
@@ -751,42 +728,42 @@ __global__ void __launch_bounds__(THREADS, 1)
         ck *= scale_log2;
         // columns below cmin do not see this key (row = rb ROWS + column, position row / G)
         cmin = key >= m.valid ? NC : max(m.joff + key, 0) * G - m.rb * L::ROWS - (PAIR ? w * NR : 0) - c0;
-        if (first) {
-          // the queries' scales, and no maximum yet (each warp writes the same for itself)
-          const float* cq = (const float*)(sQ + (m.flags & kQSlot ? L::Q_BUF : 0) + 2 * L::ROWS * D) +
-                            (PAIR ? w * NR : 0) + c0;
+        if (!first) {
+          // (a hidden key's exponent may raise a false alarm, which only costs time)
+          const tc::F2 ck2 = tc::f2(ck, ck);
+          float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < NC; ++j) e[j] *= ck * cq[j];
-        } else {
-          const float2 ck2 = make_float2(ck, ck);
+          for (int j0 = 0; j0 < NC; j0 += CH) {
+            float e[CH];
+            tc::tmem_ld(t_s + j0, e);
 #pragma unroll
-          for (int j = 0; j < NC; j += 2) {
-            const float4 cm = *(const float4*)&col[j];
-            const float2 x = tc::ffma2(tc::fmul2(make_float2(e[j], e[j + 1]), ck2), make_float2(cm.x, cm.z),
-                                       make_float2(cm.y, cm.w));
-            e[j] = x.x, e[j + 1] = x.y;
+            for (int j = 0; j < CH; j += 4) {
+              const ulonglong2 q = *(const ulonglong2*)&cqs[j0 + j], nm = *(const ulonglong2*)&nms[j0 + j];
+              float x, y;
+              tc::f2_get(tc::f2_fma(tc::f2_mul(tc::f2(e[j], e[j + 1]), ck2), q.x, nm.x), x, y);
+              mx[0] = fmaxf(fmaxf(mx[0], x), y);
+              tc::f2_get(tc::f2_fma(tc::f2_mul(tc::f2(e[j + 2], e[j + 3]), ck2), q.y, nm.y), x, y);
+              mx[1] = fmaxf(fmaxf(mx[1], x), y);
+            }
           }
+          e_max = key < m.valid ? fmaxf(mx[0], mx[1]) : -INFINITY;
         }
-        if (cmin > 0) {
-#pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (j < cmin) e[j] = -INFINITY;
-        }
-        float mx[4] = {e[0], e[1], e[2], e[3]};
-#pragma unroll
-        for (int j = 4; j < NC; j += 4)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], e[j + k]);
-        e_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       }
       if (group_or(!run || first || e_max > kMaxExp || sv > Mv)) {
-        // The maxima move (or the group leaves).  s = e + m (e alone in a first tile).
+        // The maxima move (or the group leaves).
+        const float* cq = (const float*)(sQ + (m.flags & kQSlot ? L::Q_BUF : 0) + 2 * L::ROWS * D) +
+                          (PAIR ? w * NR : 0) + c0;  // the queries' scales (in place during a first tile)
         if (run) {
+#pragma unroll 1
+          for (int j0 = 0; j0 < NC; j0 += 8) {
+            float v[8];
+            tc::tmem_ld(t_s + j0, v);
 #pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            if (!first) e[j] -= col[j].y;
-            const int top = __reduce_max_sync(0xffffffffu, float_key(e[j]));
-            if (lane == j) ms.cmax[gq][quarter][j] = key_float(top);
+            for (int j = 0; j < 8; ++j) {
+              const float x = j0 + j < cmin ? -INFINITY : v[j] * ck * (first ? cq[j0 + j] : cqs[j0 + j]);
+              const int top = __reduce_max_sync(0xffffffffu, float_key(x));
+              if (lane == j) ms.cmax[gq][quarter][j0 + j] = key_float(top);
+            }
           }
           const float t = warp_max(sv);
           if (lane == 0) ms.svmax[gq][quarter] = t;
@@ -797,11 +774,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           const float cm =
               fmaxf(fmaxf(ms.cmax[gq][0][j], ms.cmax[gq][1][j]), fmaxf(ms.cmax[gq][2][j], ms.cmax[gq][3][j]));
           const float m_old = first ? -INFINITY : ms.m[gq][j], m_new = fmaxf(m_old, cm);
-          const float cq = first ? ((const float*)(sQ + (m.flags & kQSlot ? L::Q_BUF : 0) + 2 * L::ROWS * D))
-                                       [(PAIR ? w * NR : 0) + c0 + j]
-                                 : col[j].x;
           ms.m[gq][j] = m_new;
-          col[j] = make_float2(cq, m_new == -INFINITY ? 0.f : -m_new);
+          if (first) cqs[j] = cq[j];
+          nms[j] = m_new == -INFINITY ? 0.f : -m_new;
           alpha[j] = m_old == -INFINITY ? 1.f : exp2f(m_old - m_new);
         }
         const float sv_top = fmaxf(fmaxf(ms.svmax[gq][0], ms.svmax[gq][1]), fmaxf(ms.svmax[gq][2], ms.svmax[gq][3]));
@@ -809,13 +784,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float mv_ratio = mv_new > 0.f ? Mv / mv_new : 0.f;
         Mv = mv_new;
         inv_mv = Mv > 0.f ? fminf(1.f / Mv, 3.402823466e38f) : 0.f;
-        group_or(false);  // col, m and alpha are written
+        group_or(false);  // cq, nm, m and alpha are written
         if (first) {
 #pragma unroll
-          for (int j = 0; j < NC; ++j) l[j] = 0.f;
+          for (int j = 0; j < NC / 2; ++j) l2[j] = 0;
         } else {
 #pragma unroll
-          for (int j = 0; j < NC; ++j) l[j] *= alpha[j];
+          for (int j = 0; j < NC / 2; ++j) l2[j] = tc::f2_mul(l2[j], *(const tc::F2*)&alpha[2 * j]);
           // O^T holds the side's earlier tiles of the piece once its last product is done
           ok = wait(&ms.pv_done[w], (n - 1) & 1);
           if (ok) {
@@ -835,8 +810,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
         }
-#pragma unroll
-        for (int j = 0; j < NC; ++j) e[j] += col[j].y;
       }
       // From here on a failed wait only skips work; the group leaves at the next barrier.
       // The side's last product is done: its P buffer is free, and O^T is complete if the
@@ -867,8 +840,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int q = 0; q < D / 16; ++q)
               *(uint4*)(v_row + h * blk_rows(a.K) * D + q * 16) = make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (j >= cmin) l[j] = __int_as_float(0x7fffffff);
+          for (int j = 0; j < NC; j += 2) {
+            float x, y;
+            tc::f2_get(l2[j / 2], x, y);
+            if (j >= cmin) x = __int_as_float(0x7fffffff);
+            if (j + 1 >= cmin) y = __int_as_float(0x7fffffff);
+            l2[j / 2] = tc::f2(x, y);
+          }
         }
       }
       // V rows past the last key may hold anything (their weights are 0): clear them
@@ -877,30 +855,43 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int q = 0; q < D / 16; ++q) *(uint4*)(v_row + q * 16) = make_uint4(0, 0, 0, 0);
       }
       const float rv = sv * inv_mv * kPScale;
-      const float2 rv2 = make_float2(rv, rv);
+      const tc::F2 rv2 = tc::f2(rv, rv);
       uint8_t* prow = sP + w * L::P_BUF + key * 128;
-      constexpr int CH = NC % 16 == 0 ? 16 : 8;
+      const tc::F2 ck2 = tc::f2(ck, ck);
 #pragma unroll
       for (int j0 = 0; j0 < NC; j0 += CH) {
+        float e[CH];
+        tc::tmem_ld(t_s + j0, e);
+        if (j0 + CH == NC) {  // S is read
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&ms.s_free[b]);
+        }
+#pragma unroll
+        for (int j = 0; j < CH; j += 4) {
+          const ulonglong2 q = *(const ulonglong2*)&cqs[j0 + j], nm = *(const ulonglong2*)&nms[j0 + j];
+          tc::f2_get(tc::f2_fma(tc::f2_mul(tc::f2(e[j], e[j + 1]), ck2), q.x, nm.x), e[j], e[j + 1]);
+          tc::f2_get(tc::f2_fma(tc::f2_mul(tc::f2(e[j + 2], e[j + 3]), ck2), q.y, nm.y), e[j + 2], e[j + 3]);
+        }
+        if (cmin > j0) {
+#pragma unroll
+          for (int j = 0; j < CH; ++j)
+            if (j0 + j < cmin) e[j] = -INFINITY;
+        }
         uint32_t hi[CH / 4], lo[CH / 4];
 #pragma unroll
         for (int q = 0; q < CH / 4; ++q) {
-          uint32_t hh[2], ll[2];
+          __half2 ph[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int j = j0 + 4 * q + 2 * k;
-            const float2 p = make_float2(tc::ex2_ftz(e[j]), tc::ex2_ftz(e[j + 1]));
-            const float2 ls = tc::fadd2(make_float2(l[j], l[j + 1]), p);
-            l[j] = ls.x, l[j + 1] = ls.y;
-            const float2 pv = tc::fmul2(p, rv2);
-            // fp16 first (11 bits, well below the two parts' error): the parts' difference
-            // is then packed half arithmetic
-            const __half2 ph = __floats2half2_rn(pv.x, pv.y);
-            hh[k] = e4m3x2_h(ph);
-            ll[k] = e4m3x2_h(__hmul2(__hsub2(ph, e4m3x2_to_h2(hh[k])), __float2half2_rn(kLoScale)));
+            const int j = 4 * q + 2 * k;
+            const tc::F2 p = tc::f2(tc::ex2_ftz(e[j]), tc::ex2_ftz(e[j + 1]));
+            l2[(j0 + j) / 2] = tc::f2_add(l2[(j0 + j) / 2], p);
+            float x, y;
+            tc::f2_get(tc::f2_mul(p, rv2), x, y);
+            ph[k] = __floats2half2_rn(x, y);
           }
-          hi[q] = hh[0] | (hh[1] << 16);
-          lo[q] = ll[0] | (ll[1] << 16);
+          split_weights(ph[0], ph[1], hi[q], lo[q]);
         }
         // byte c0 + j0 of the row's high half, and of its low half 64 bytes on
         const int ch = (c0 + j0) / 16;
@@ -926,11 +917,33 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int rows = min(NC, min(L::ROWS, R - m.rb * L::ROWS) - (PAIR ? w * NR : 0) - c0);
         const size_t base =
             (PAIR ? (size_t)m.slot * RB + w * NR : ((size_t)m.slot * 2 + (m.flags & kHalf ? 1 : 0)) * RB) + c0;
+        // l summed over the lanes: while the count is even, a lane keeps one half of the
+        // columns and hands the other half to its partner
+        float l[NC];
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-          const float t = warp_sum(l[j]);
-          if (lane == j) ms.cmax[gq][quarter][j] = t;
+        for (int j = 0; j < NC; j += 2) tc::f2_get(l2[j / 2], l[j], l[j + 1]);
+        int cnt = NC, cc = 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const bool up = (lane & o) != 0;
+          if (cnt % 2 == 0) {
+            cnt /= 2;
+#pragma unroll
+            for (int j = 0; j < NC / 2; ++j)
+              if (j < cnt) {
+                const float give = up ? l[j] : l[j + cnt], keep = up ? l[j + cnt] : l[j];
+                l[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+              }
+            cc += up ? cnt : 0;
+          } else {
+#pragma unroll
+            for (int j = 0; j < NC / 2; ++j)
+              if (j < cnt) l[j] += __shfl_xor_sync(0xffffffffu, l[j], o);
+          }
         }
+#pragma unroll
+        for (int j = 0; j < NC / 2; ++j)
+          if (j < cnt) ms.cmax[gq][quarter][cc + j] = l[j];
         group_or(false);
         if (quarter == 0 && lane < rows) {
           float* ml = a.ws_ml + (base + lane) * 2;
@@ -994,15 +1007,15 @@ bool launch(const AttnKv8Args& a, int grid, cudaStream_t s) {
     set_error("cudaFuncSetAttribute(attn_kv8_tc_kernel) failed");
     return false;
   }
-  int box_rows = 16;
-  while (box_rows < TT && a.kv.page_size % (2 * box_rows) == 0) box_rows *= 2;
+  int box_shift = 4;  // boxes of the largest power of two of rows that divides the page, up to a tile
+  while ((1 << box_shift) < TT && a.kv.page_size % (2 << box_shift) == 0) ++box_shift;
   Maps maps;
-  if (!make_map(&maps.k, a.kv, a.kv.k, box_rows) || !make_map(&maps.v, a.kv, a.kv.v, box_rows)) {
+  if (!make_map(&maps.k, a.kv, a.kv.k, 1 << box_shift) || !make_map(&maps.v, a.kv, a.kv.v, 1 << box_shift)) {
     set_error("cuTensorMapEncodeTiled failed for the 8-bit cache");
     return false;
   }
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
-  launch_pdl(kernel, grid, THREADS, L::SMEM, s, maps, a, scale_log2, box_rows);
+  launch_pdl(kernel, grid, THREADS, L::SMEM, s, maps, a, scale_log2, box_shift);
   note_launch();
   return true;
 }
