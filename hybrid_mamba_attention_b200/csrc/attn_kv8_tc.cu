@@ -48,14 +48,22 @@ namespace hspec {
 namespace {
 
 constexpr int TT = kAttn8Tile;  // keys per tile
-constexpr int NPW = 2;          // producer warps
-constexpr int SM_WARP0 = 4;     // first softmax warp (a multiple of 4: warp % 4 is its TMEM quarter)
 constexpr int SMW = 16;         // softmax warps: four groups of four
-constexpr int THREADS = 32 * (SM_WARP0 + SMW);
-// registers per thread after the launch's 96: 128 * 64 + 512 * 104 = 640 * 96
-constexpr int kFewRegs = 64, kManyRegs = 104;
+// Warps and registers by the width of the query side.  Up to 32 columns a producer pair's
+// instructions from tile to tile are the longest of the chain, so two pairs take turns; with
+// more columns the softmax is, and its threads need the registers that a second pair would
+// take (64 columns: 850 us with one pair, 967 with two at 128 requests of 16 positions;
+// 8 columns: 459 and 415 at 64 requests of one).  setmaxnreg moves registers inside what the
+// launch gives, THREADS * LAUNCH: 256 * 48 + 512 * 96 = 768 * 80, 128 * 56 + 512 * 104 < 640 * 96.
+template <int NR>
+struct Warps {
+  static constexpr int NPW = NR <= 32 ? 4 : 2;     // producer warps: K's and V's, per pair
+  static constexpr int SM_WARP0 = NR <= 32 ? 8 : 4;  // first softmax warp (a multiple of 4: warp % 4 is its TMEM quarter)
+  static constexpr int THREADS = 32 * (SM_WARP0 + SMW);
+  static constexpr int kFewRegs = NR <= 32 ? 48 : 56, kManyRegs = NR <= 32 ? 96 : 104;
+};
 constexpr float kPScale = 8.f;    // 2^3: weights enter P times this
-constexpr float kMaxExp = 5.f;    // a weight's exponent may reach this before the maximum moves
+constexpr float kOver = 32.f;     // 2^5: a weight may reach this before the maximum moves (P: 2^8 of e4m3's 448)
 constexpr float kLoScale = 16.f;  // the low part of P is held times this
 constexpr int kMaxChunksAuto = 256, kMaxChunksExplicit = 2048;
 constexpr int kBlkRows = 64;      // scales of a block's rows (K <= 64)
@@ -312,10 +320,12 @@ __device__ __forceinline__ TileMeta load_meta(const TileMeta* m) {
 // = tile.  PAIR = true (up to 128 rows): each takes one half of the rows of every tile,
 // tile = item / 2, so that a tile's bytes serve both halves.
 template <int D, int NR, bool PAIR>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
     attn_kv8_tc_kernel(const __grid_constant__ Maps maps, const AttnKv8Args a, float scale_log2, int box_shift) {
   using L = Lay<D, NR, PAIR>;
   constexpr int NS = L::NS, PN = L::PN, NC = NR / 2;
+  constexpr int NPW = Warps<NR>::NPW, SM_WARP0 = Warps<NR>::SM_WARP0;
+  constexpr int kFewRegs = Warps<NR>::kFewRegs, kManyRegs = Warps<NR>::kManyRegs;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023) & ~1023u) - raw);
@@ -337,7 +347,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      tc::mbar_init(&ms.kv_full[s], NPW + 16);  // a lane of each producer warp, the scale lanes
+      tc::mbar_init(&ms.kv_full[s], 18);  // of K's and V's warp one lane and eight scale lanes each
       tc::mbar_init(&ms.kv_empty[s], 1);
     }
     for (int b = 0; b < 4; ++b) {
@@ -366,11 +376,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp < NPW) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     // ------------------------------------------------------------ producers
-    // Warp 0 brings K, warp 1 V: lane x < 8 the tile's box x of 2^box_shift rows (within one
-    // page each), lane 8 + i the scale of its 16-key group i.  Both walk the same tiles;
-    // warp 0 also loads the queries and describes the tile.  (One warp's instructions from
-    // tile to tile bound the whole kernel when R is small: the loop is kept short.)
-    const int pw = warp;
+    // Warps 0 and 1 bring K and V (of the even tiles, and warps 2 and 3 of the odd ones): lane
+    // x < 8 the tile's box x of 2^box_shift rows (within one page each), lane 8 + i the
+    // scale of its 16-key group i.  All walk the same tiles; the K warp describes its tile,
+    // warp 0 also loads the queries.
+    const int pw = warp & 1, pair = warp >> 1;
     const int sub = lane < 8 ? lane << box_shift : 16 * (lane & 7);  // first key of the tile that concerns the lane
     const CUtensorMap* map = pw == 1 ? &maps.v : &maps.k;
     const float* scales = pw == 1 ? a.kv.vs : a.kv.ks;
@@ -456,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int qslot = seq % L::NQ, quse = seq / L::NQ;
 
       // the piece's queries into buffer `qslot` once the piece before in it is done
-      if (pw == 0) {
+      if (warp == 0) {
         if (lane == 0) {
           ok = tc::mbar_wait(&ms.q_empty[qslot], (quse & 1) ^ 1, err, lim);
           if (ok) {
@@ -477,6 +487,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           base = page_index((pc.lt0 + local) * TT);
           if (local + 4 < n_tiles) ids_ahead = window(pc, local / 4 + 1);
         }
+        if (NPW == 2 || (tile_i & 1) == pair) {
         const int st = pc.lt0 + local;  // tile of the sequence
         const int t0 = st * TT;
         const bool block = st >= ct;
@@ -523,6 +534,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::tma_load_3d_hint(dst + sub * D, map, &ms.kv_full[s], 0, tk - pidx * page, row, once);
         }
         __syncwarp();
+        }
         ++tile_i;
         if (++s == NS) s = 0, s_par ^= 1;
         if (local == 0) {  // look ahead while the ring is full
@@ -541,8 +553,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::mbar_wait(&ms.q_full[q % L::NQ], (q / L::NQ) & 1, err);
     }
     __syncwarp();
+    tc::bar_or<1, 32 * NPW>(false);  // (all have seen their stages' last fillings)
     // sentinel stage: no more work
-    if (!stopped) {
+    if (!stopped && pair == 0) {
       if (tc::mbar_wait_warp(&ms.kv_empty[s], s_par, err, lim) && lane < 9) {  // as many arrivals as a tile's
         if (threadIdx.x == 0) ms.meta[s].flags = kEnd;
         tc::mbar_arrive(&ms.kv_full[s]);
@@ -701,6 +714,83 @@ __global__ void __launch_bounds__(THREADS, 1)
       pend = false;
     };
 
+    // Exponents e = s - m of CH columns from j0 on: s = S (key scale) (query scale).
+    auto exponents = [&](uint32_t t_s, int j0, tc::F2 ck2, int cmin, float (&e)[CH]) {
+      tc::tmem_ld(t_s + j0, e);
+#pragma unroll
+      for (int j = 0; j < CH; j += 4) {
+        const ulonglong2 q = *(const ulonglong2*)&cqs[j0 + j], nm = *(const ulonglong2*)&nms[j0 + j];
+        tc::f2_get(tc::f2_fma(tc::f2_mul(tc::f2(e[j], e[j + 1]), ck2), q.x, nm.x), e[j], e[j + 1]);
+        tc::f2_get(tc::f2_fma(tc::f2_mul(tc::f2(e[j + 2], e[j + 3]), ck2), q.y, nm.y), e[j + 2], e[j + 3]);
+      }
+      if (cmin > j0) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+          if (j0 + j < cmin) e[j] = -INFINITY;
+      }
+    };
+    // The key's weights 2^e, added to the sums and stored in two parts, times rv, as its row
+    // of P.  `over` becomes the largest of them.
+    float over = 0.f;
+    auto weigh = [&](uint32_t t_s, float ck, float rv, int cmin) {
+      const tc::F2 ck2 = tc::f2(ck, ck), rv2 = tc::f2(rv, rv);
+      uint8_t* prow = sP + w * L::P_BUF + key * 128;
+      float top[2] = {0.f, 0.f};
+#pragma unroll
+      for (int j0 = 0; j0 < NC; j0 += CH) {
+        float e[CH];
+        exponents(t_s, j0, ck2, cmin, e);
+        uint32_t hi[CH / 4], lo[CH / 4];
+#pragma unroll
+        for (int q = 0; q < CH / 4; ++q) {
+          __half2 ph[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int j = 4 * q + 2 * k;
+            const float x = tc::ex2_ftz(e[j]), y = tc::ex2_ftz(e[j + 1]);
+            top[k] = fmaxf(fmaxf(top[k], x), y);
+            const tc::F2 p = tc::f2(x, y);
+            l2[(j0 + j) / 2] = tc::f2_add(l2[(j0 + j) / 2], p);
+            float u, v;
+            tc::f2_get(tc::f2_mul(p, rv2), u, v);
+            ph[k] = __floats2half2_rn(u, v);
+          }
+          split_weights(ph[0], ph[1], hi[q], lo[q]);
+        }
+        // byte c0 + j0 of the row's high half, and of its low half 64 bytes on
+        const int ch = (c0 + j0) / 16;
+        if constexpr (CH == 16) {
+          *(uint4*)(prow + ((ch ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *(uint4*)(prow + (((4 + ch) ^ (key & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        } else {
+          const int in = (c0 + j0) & 8;
+          *(uint2*)(prow + ((ch ^ (key & 7)) << 4) + in) = make_uint2(hi[0], hi[1]);
+          *(uint2*)(prow + (((4 + ch) ^ (key & 7)) << 4) + in) = make_uint2(lo[0], lo[1]);
+        }
+      }
+      over = fmaxf(top[0], top[1]);
+    };
+    // Takes the weights that weigh() added out of the sums again.  What a sum loses by that is
+    // 2^-24 of the weight, which is the new maximum's at most; a weight that overflowed
+    // leaves a new maximum beside which the earlier sum is nothing.
+    auto unsum = [&](uint32_t t_s, float ck, int cmin) {
+      const tc::F2 ck2 = tc::f2(ck, ck);
+#pragma unroll
+      for (int j0 = 0; j0 < NC; j0 += CH) {
+        float e[CH];
+        exponents(t_s, j0, ck2, cmin, e);
+#pragma unroll
+        for (int j = 0; j < CH; j += 2) {
+          const float x = tc::ex2_ftz(e[j]), y = tc::ex2_ftz(e[j + 1]);
+          float u, v;
+          tc::f2_get(l2[(j0 + j) / 2], u, v);
+          u = x < INFINITY ? u - x : x > 0.f ? 0.f : u;
+          v = y < INFINITY ? v - y : y > 0.f ? 0.f : v;
+          l2[(j0 + j) / 2] = tc::f2(u, v);
+        }
+      }
+    };
+
     int n = 0;  // items of the side so far
     int s = PAIR ? 0 : w;  // the item's stage
     for (;; ++n) {
@@ -711,7 +801,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       int cmin = 0;
       bool first = false;
       float ck = 0.f, sv = 0.f;
-      float e_max = -INFINITY;
       const uint32_t t_s = tmem + lane_off + L::S_COL(b) + c0;
       if (run) {
         tc::tc_fence_after();
@@ -728,39 +817,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         ck *= scale_log2;
         // columns below cmin do not see this key (row = rb ROWS + column, position row / G)
         cmin = key >= m.valid ? NC : max(m.joff + key, 0) * G - m.rb * L::ROWS - (PAIR ? w * NR : 0) - c0;
-        if (!first) {
-          // (a hidden key's exponent may raise a false alarm, which only costs time)
-          const tc::F2 ck2 = tc::f2(ck, ck);
-          float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-          for (int j0 = 0; j0 < NC; j0 += CH) {
-            float e[CH];
-            tc::tmem_ld(t_s + j0, e);
-#pragma unroll
-            for (int j = 0; j < CH; j += 4) {
-              const ulonglong2 q = *(const ulonglong2*)&cqs[j0 + j], nm = *(const ulonglong2*)&nms[j0 + j];
-              float x, y;
-              tc::f2_get(tc::f2_fma(tc::f2_mul(tc::f2(e[j], e[j + 1]), ck2), q.x, nm.x), x, y);
-              mx[0] = fmaxf(fmaxf(mx[0], x), y);
-              tc::f2_get(tc::f2_fma(tc::f2_mul(tc::f2(e[j + 2], e[j + 3]), ck2), q.y, nm.y), x, y);
-              mx[1] = fmaxf(fmaxf(mx[1], x), y);
-            }
-          }
-          e_max = key < m.valid ? fmaxf(mx[0], mx[1]) : -INFINITY;
-        }
       }
-      if (group_or(!run || first || e_max > kMaxExp || sv > Mv)) {
+      // The weights are computed under the maxima so far; only if one of them then exceeds
+      // kOver (or a V scale the largest so far) do the maxima move and the tile's weights
+      // get computed again.  A first tile has no maxima yet.  The side's last product must be
+      // done: its P buffer is free then, and O^T complete.
+      if (run && n > 0) ok = wait(&ms.pv_done[w], (n - 1) & 1);
+      if (run && ok && pend) write_partial();  // (before this item's product may overwrite it)
+      bool fresh = first, moved = false, leave = false;
+      while (true) {
+        if (run && ok && !fresh) weigh(t_s, ck, sv * inv_mv * kPScale, cmin);
+        if (!group_or(!run || !ok || fresh || (!moved && (over > kOver || sv > Mv)))) break;
         // The maxima move (or the group leaves).
         const float* cq = (const float*)(sQ + (m.flags & kQSlot ? L::Q_BUF : 0) + 2 * L::ROWS * D) +
                           (PAIR ? w * NR : 0) + c0;  // the queries' scales (in place during a first tile)
-        if (run) {
+        if (run && ok) {
+          if (!fresh) unsum(t_s, ck, cmin);
 #pragma unroll 1
           for (int j0 = 0; j0 < NC; j0 += 8) {
             float v[8];
             tc::tmem_ld(t_s + j0, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float x = j0 + j < cmin ? -INFINITY : v[j] * ck * (first ? cq[j0 + j] : cqs[j0 + j]);
+              const float x = j0 + j < cmin ? -INFINITY : v[j] * ck * (fresh ? cq[j0 + j] : cqs[j0 + j]);
               const int top = __reduce_max_sync(0xffffffffu, float_key(x));
               if (lane == j) ms.cmax[gq][quarter][j0 + j] = key_float(top);
             }
@@ -768,55 +847,56 @@ __global__ void __launch_bounds__(THREADS, 1)
           const float t = warp_max(sv);
           if (lane == 0) ms.svmax[gq][quarter] = t;
         }
-        if (group_or(!run)) break;
+        if (group_or(!run || !ok)) {
+          leave = true;
+          break;
+        }
         if (quarter == 0 && lane < NC) {
           const int j = lane;
           const float cm =
               fmaxf(fmaxf(ms.cmax[gq][0][j], ms.cmax[gq][1][j]), fmaxf(ms.cmax[gq][2][j], ms.cmax[gq][3][j]));
-          const float m_old = first ? -INFINITY : ms.m[gq][j], m_new = fmaxf(m_old, cm);
+          const float m_old = fresh ? -INFINITY : ms.m[gq][j], m_new = fmaxf(m_old, cm);
           ms.m[gq][j] = m_new;
-          if (first) cqs[j] = cq[j];
+          if (fresh) cqs[j] = cq[j];
           nms[j] = m_new == -INFINITY ? 0.f : -m_new;
           alpha[j] = m_old == -INFINITY ? 1.f : exp2f(m_old - m_new);
         }
         const float sv_top = fmaxf(fmaxf(ms.svmax[gq][0], ms.svmax[gq][1]), fmaxf(ms.svmax[gq][2], ms.svmax[gq][3]));
-        const float mv_new = first ? sv_top : fmaxf(Mv, sv_top);
+        const float mv_new = fresh ? sv_top : fmaxf(Mv, sv_top);
         const float mv_ratio = mv_new > 0.f ? Mv / mv_new : 0.f;
         Mv = mv_new;
         inv_mv = Mv > 0.f ? fminf(1.f / Mv, 3.402823466e38f) : 0.f;
         group_or(false);  // cq, nm, m and alpha are written
-        if (first) {
+        if (fresh) {
 #pragma unroll
           for (int j = 0; j < NC / 2; ++j) l2[j] = 0;
         } else {
 #pragma unroll
           for (int j = 0; j < NC / 2; ++j) l2[j] = tc::f2_mul(l2[j], *(const tc::F2*)&alpha[2 * j]);
-          // O^T holds the side's earlier tiles of the piece once its last product is done
-          ok = wait(&ms.pv_done[w], (n - 1) & 1);
-          if (ok) {
-            tc::tc_fence_after();
+          // O^T holds the side's earlier tiles of the piece
+          tc::tc_fence_after();
 #pragma unroll 1
-            for (int j0 = 0; j0 < NC; j0 += 8) {
-              float o[8], p[8];
-              tc::tmem_ld(t_hi + j0, o);
-              tc::tmem_ld(t_lo + j0, p);
+          for (int j0 = 0; j0 < NC; j0 += 8) {
+            float o[8], p[8];
+            tc::tmem_ld(t_hi + j0, o);
+            tc::tmem_ld(t_lo + j0, p);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float f = alpha[j0 + j] * mv_ratio;
-                o[j] *= f, p[j] *= f;
-              }
-              tc::tmem_st8(t_hi + j0, o);
-              tc::tmem_st8(t_lo + j0, p);
+            for (int j = 0; j < 8; ++j) {
+              const float f = alpha[j0 + j] * mv_ratio;
+              o[j] *= f, p[j] *= f;
             }
+            tc::tmem_st8(t_hi + j0, o);
+            tc::tmem_st8(t_lo + j0, p);
           }
         }
+        fresh = false, moved = true;
       }
-      // From here on a failed wait only skips work; the group leaves at the next barrier.
-      // The side's last product is done: its P buffer is free, and O^T is complete if the
-      // previous piece's partial is still to be written (before this item's product may
-      // overwrite it).
-      if (ok && n > 0) ok = wait(&ms.pv_done[w], (n - 1) & 1);
-      if (ok && pend) write_partial();
+      if (leave) break;
+      // From here on nothing waits: the item is complete.
+      // S is read
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&ms.s_free[b]);
       uint8_t* v_row = sKV + s * L::STAGE + L::KV + key * D;
       if (m.flags & kMixed) {
         // a NaN in a V row that some column does not see: the product would carry it into
@@ -853,58 +933,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!(m.flags & kBlock) && key >= m.valid && key < ((m.valid + 31) & ~31)) {
 #pragma unroll 1
         for (int q = 0; q < D / 16; ++q) *(uint4*)(v_row + q * 16) = make_uint4(0, 0, 0, 0);
-      }
-      const float rv = sv * inv_mv * kPScale;
-      const tc::F2 rv2 = tc::f2(rv, rv);
-      uint8_t* prow = sP + w * L::P_BUF + key * 128;
-      const tc::F2 ck2 = tc::f2(ck, ck);
-#pragma unroll
-      for (int j0 = 0; j0 < NC; j0 += CH) {
-        float e[CH];
-        tc::tmem_ld(t_s + j0, e);
-        if (j0 + CH == NC) {  // S is read
-          tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&ms.s_free[b]);
-        }
-#pragma unroll
-        for (int j = 0; j < CH; j += 4) {
-          const ulonglong2 q = *(const ulonglong2*)&cqs[j0 + j], nm = *(const ulonglong2*)&nms[j0 + j];
-          tc::f2_get(tc::f2_fma(tc::f2_mul(tc::f2(e[j], e[j + 1]), ck2), q.x, nm.x), e[j], e[j + 1]);
-          tc::f2_get(tc::f2_fma(tc::f2_mul(tc::f2(e[j + 2], e[j + 3]), ck2), q.y, nm.y), e[j + 2], e[j + 3]);
-        }
-        if (cmin > j0) {
-#pragma unroll
-          for (int j = 0; j < CH; ++j)
-            if (j0 + j < cmin) e[j] = -INFINITY;
-        }
-        uint32_t hi[CH / 4], lo[CH / 4];
-#pragma unroll
-        for (int q = 0; q < CH / 4; ++q) {
-          __half2 ph[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int j = 4 * q + 2 * k;
-            const tc::F2 p = tc::f2(tc::ex2_ftz(e[j]), tc::ex2_ftz(e[j + 1]));
-            l2[(j0 + j) / 2] = tc::f2_add(l2[(j0 + j) / 2], p);
-            float x, y;
-            tc::f2_get(tc::f2_mul(p, rv2), x, y);
-            ph[k] = __floats2half2_rn(x, y);
-          }
-          split_weights(ph[0], ph[1], hi[q], lo[q]);
-        }
-        // byte c0 + j0 of the row's high half, and of its low half 64 bytes on
-        const int ch = (c0 + j0) / 16;
-        if (ok) {
-          if constexpr (CH == 16) {
-            *(uint4*)(prow + ((ch ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *(uint4*)(prow + (((4 + ch) ^ (key & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          } else {
-            const int in = (c0 + j0) & 8;
-            *(uint2*)(prow + ((ch ^ (key & 7)) << 4) + in) = make_uint2(hi[0], hi[1]);
-            *(uint2*)(prow + (((4 + ch) ^ (key & 7)) << 4) + in) = make_uint2(lo[0], lo[1]);
-          }
-        }
       }
       tc::fence_proxy_async();
       tc::tc_fence_before();
@@ -1015,7 +1043,7 @@ bool launch(const AttnKv8Args& a, int grid, cudaStream_t s) {
     return false;
   }
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
-  launch_pdl(kernel, grid, THREADS, L::SMEM, s, maps, a, scale_log2, box_shift);
+  launch_pdl(kernel, grid, Warps<NR>::THREADS, L::SMEM, s, maps, a, scale_log2, box_shift);
   note_launch();
   return true;
 }
