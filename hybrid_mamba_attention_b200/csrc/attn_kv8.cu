@@ -181,32 +181,9 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const AttnKv8Args a
   const int g = h / G, row = j * G + h % G;
   const int ctx = a.ctx_lens[c];
   const bool valid = live && ctx >= 0 && ctx <= (long)a.kv.max_pages * a.kv.page_size;
-  // The row's partials q = 0 .. ns - 1 at rows base0 + q * stride.  CUDA-core path: one per
-  // split of (c, g).  Tensor-core path: the sequence (c, rb, g) holds t_seq tiles from unit
-  // s0 of the line, which is cut into chunks of Z units; its piece in chunk k0 + p has slot
-  // c * spr + rb * Hkv + g + k0 + p, one partial (pair) or two, q = 2 p + half: half h holds
-  // the piece's tiles of parity h and exists iff the piece has more than h tiles.
-  int ns = 0, s0 = 0, k0 = 0, t_seq = 0, Z = 1;
-  const int halves = a.tc && !a.pair ? 2 : 1;
-  size_t base0, stride = R;
-  if (a.tc) {
-    const int* off = a.sched + 64;
-    const int spr = Hkv * a.n_rb;
-    const int rb = row / a.row_block, r = rb * Hkv + g;
-    Z = a.sched[2];
-    if (valid) {
-      const int tw = (off[c + 1] - off[c]) / spr;
-      t_seq = tw - kAttn8SeqUnits;
-      s0 = off[c] + r * tw + kAttn8SeqUnits;
-      k0 = s0 / Z;
-      ns = t_seq > 0 ? halves * ((s0 + t_seq - 1) / Z - k0 + 1) : 0;
-    }
-    stride = R < a.row_block ? R : a.row_block;
-    base0 = ((size_t)c * spr + r + k0) * halves * stride + row % a.row_block;
-  } else {
-    ns = valid ? (ctx + (a.kb ? a.K : 0) + a.split_tokens - 1) / a.split_tokens : 0;
-    base0 = ((size_t)c * Hkv + g) * a.n_splits * R + row;
-  }
+  // The row's partials, one per split of (c, g).
+  const int ns = valid ? (ctx + (a.kb ? a.K : 0) + a.split_tokens - 1) / a.split_tokens : 0;
+  const size_t base0 = ((size_t)c * Hkv + g) * a.n_splits * R + row, stride = R;
   float M = -INFINITY, L = 0.f, o[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) o[i] = 0.f;
@@ -220,10 +197,6 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const AttnKv8Args a
     M = mn;
   };
   for (int q = wq; q < ns; q += W) {
-    if (halves == 2) {
-      const int lo = max(s0, (k0 + (q >> 1)) * Z), hi = min(s0 + t_seq, (k0 + (q >> 1) + 1) * Z);
-      if (hi - lo <= (q & 1)) continue;
-    }
     const size_t b = base0 + (size_t)q * stride;
     const float2 ml = *(const float2*)(a.ws_ml + b * 2);
     const float* acc = a.ws_acc + b * D;
@@ -320,12 +293,9 @@ size_t attn_kv8_ws_bytes(int dtype, int C, int K, int Hq, const Kv8& kv, int spl
 }
 
 bool attn_kv8(int dtype, AttnKv8Args& a, int split_req, void* ws, cudaStream_t s) {
-  a.tc = attn_kv8_tc_shape(dtype, a.kv.D, a.kv.page_size);
-  if (a.tc) {
+  if (attn_kv8_tc_shape(dtype, a.kv.D, a.kv.page_size)) {
     attn_kv8_tc_plan(a, split_req, ws);
-    if (!attn_kv8_tc_launch(a, s)) return false;
-    launch_merge<bf16>(a, s);
-    return true;
+    return attn_kv8_tc_launch(a, s);
   }
   const int G = a.Hq / a.kv.Hkv;
   const Split sp = split_of(a.C, a.K, G, a.kv, split_req);

@@ -165,10 +165,11 @@ __device__ __forceinline__ float row_factor(float m, float& inv) {
   return __int_as_float((254 + 7 - e) << 23);
 }
 
-// CTA 0: the line's offsets and the partition.  The others: two-part images, one warp per
-// row: query rows first, then the blocks' K and V rows.
+// CTA 0: the line's offsets and the partition.  The others: two-part images, D / 8 lanes a
+// row (16 bytes of it each), `passes` times 32 / (D / 8) rows a warp: query rows first, then
+// the blocks' K and V rows.
 template <int D>
-__global__ void __launch_bounds__(256) attn_kv8_prep_kernel(const AttnKv8Args a, int grid) {
+__global__ void __launch_bounds__(256) attn_kv8_prep_kernel(const AttnKv8Args a, int grid, int passes) {
   pdl_wait();  // the previous kernel on the stream is complete from here on
   pdl_trigger();
   const int Hkv = a.kv.Hkv, G = a.Hq / Hkv, R = a.K * G, NR = a.row_block;
@@ -209,60 +210,64 @@ __global__ void __launch_bounds__(256) attn_kv8_prep_kernel(const AttnKv8Args a,
     }
     return;
   }
-  const int lane = threadIdx.x & 31;
-  const long w = (long)(blockIdx.x - 1) * 8 + (threadIdx.x >> 5);
-  const long q_rows = (long)a.C * Hkv * a.n_rb * NR;
-  const int KP = blk_rows(a.K);
-  const long b_rows = a.kb ? (long)a.C * Hkv * 2 * KP : 0;
-  if (w >= q_rows + b_rows) return;
-  // four elements per lane (D = 64: half the lanes)
-  const bool on = lane * 4 < D;
-  const bf16* src = nullptr;
-  uint8_t* hi;
-  size_t lo_off;
-  float* scale;
-  int r;
-  if (w < q_rows) {
-    r = (int)(w % NR);
-    const long seq = w / NR;  // (c * n_rb + rb) * Hkv + g
-    const int g = (int)(seq % Hkv), rb = (int)(seq / Hkv % a.n_rb), c = (int)(seq / Hkv / a.n_rb);
-    const int row = rb * NR + r;
-    if (row < R) src = (const bf16*)a.q + (size_t)(c * a.K + row / G) * a.q_rs + (size_t)(g * G + row % G) * D;
-    hi = a.q_img + seq * q_img_bytes(NR, D);
-    lo_off = (size_t)NR * D;
-    scale = (float*)(hi + 2 * lo_off) + r;
-  } else {
-    const long b = w - q_rows;
-    r = (int)(b % KP);
-    const int is_v = (int)(b / KP % 2);
-    const long cg = b / KP / 2;
-    const int g = (int)(cg % Hkv);
-    const long c = cg / Hkv;
-    if (r < a.K)
-      src = (const bf16*)(is_v ? a.vb : a.kb) + (size_t)(c * a.K + r) * (is_v ? a.vb_rs : a.kb_rs) + (size_t)g * D;
-    hi = a.blk_img + (cg * 4 + 2 * is_v) * (size_t)KP * D;
-    lo_off = (size_t)KP * D;
-    scale = a.blk_scale + (cg * 2 + is_v) * kBlkRows + r;
-  }
-  float x[4] = {0.f, 0.f, 0.f, 0.f};
-  if (src && on) {
-    const uint2 v = *(const uint2*)(src + lane * 4);
-    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-  }
-  const float m = warp_max(fmaxf(fmaxf(kv8_mag(x[0]), kv8_mag(x[1])), fmaxf(kv8_mag(x[2]), kv8_mag(x[3]))));
-  float inv;
-  const float f = row_factor(m, inv);
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, part = lane % LPR;
+  const int q_rows = a.C * Hkv * a.n_rb * NR, KP = blk_rows(a.K);
+  const int rows = q_rows + (a.kb ? a.C * Hkv * 2 * KP : 0);
+  const int w0 = ((blockIdx.x - 1) * 8 + (threadIdx.x >> 5)) * passes * RPW + lane / LPR;
+  for (int p = 0; p < passes; ++p) {
+    const int w = w0 + p * RPW;
+    const bool live = w < rows;
+    const bf16* src = nullptr;
+    uint8_t* hi = nullptr;
+    size_t lo_off = 0;
+    float* scale = nullptr;
+    int r = 0;
+    if (w < q_rows) {
+      const int seq = w / NR;  // (c * n_rb + rb) * Hkv + g
+      r = w - seq * NR;
+      const int cr = seq / Hkv, g = seq - cr * Hkv, c = cr / a.n_rb, rb = cr - c * a.n_rb;
+      const int row = rb * NR + r, j = row / G;
+      if (row < R) src = (const bf16*)a.q + (size_t)(c * a.K + j) * a.q_rs + (size_t)(g * G + row - j * G) * D;
+      hi = a.q_img + (size_t)seq * q_img_bytes(NR, D);
+      lo_off = (size_t)NR * D;
+      scale = (float*)(hi + 2 * lo_off) + r;
+    } else if (live) {
+      const int b = w - q_rows, x = b / KP;  // x = (c * Hkv + g) * 2 + is_v
+      r = b - x * KP;
+      const int is_v = x & 1, cg = x >> 1, c = cg / Hkv, g = cg - c * Hkv;
+      if (r < a.K)
+        src = (const bf16*)(is_v ? a.vb : a.kb) + (size_t)(c * a.K + r) * (is_v ? a.vb_rs : a.kb_rs) + (size_t)g * D;
+      hi = a.blk_img + (size_t)x * 2 * KP * D;
+      lo_off = (size_t)KP * D;
+      scale = a.blk_scale + x * kBlkRows + r;
+    }
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (src) v = *(const uint4*)(src + part * 8);
+    const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+    float x[8], m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] *= f;
-  uint32_t h, l;
-  split4(x, h, l);
-  if (on) {
-    const uint32_t o = swz<D>(r, lane >> 2) + (lane & 3) * 4;
-    *(uint32_t*)(hi + o) = h;
-    *(uint32_t*)(hi + lo_off + o) = l;
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(vs[i] << 16), x[2 * i + 1] = __uint_as_float(vs[i] & 0xFFFF0000u);
+      m = fmaxf(m, fmaxf(kv8_mag(x[2 * i]), kv8_mag(x[2 * i + 1])));
+    }
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float inv;
+    const float f = row_factor(m, inv);
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float y[4] = {x[4 * i] * f, x[4 * i + 1] * f, x[4 * i + 2] * f, x[4 * i + 3] * f};
+      split4(y, h[i], l[i]);
+    }
+    if (live) {
+      const uint32_t o = swz<D>(r, part >> 1) + (part & 1) * 8;
+      *(uint2*)(hi + o) = make_uint2(h[0], h[1]);
+      *(uint2*)(hi + lo_off + o) = make_uint2(l[0], l[1]);
+      if (part == 0) *scale = inv;
+    }
   }
-  if (lane == 0) *scale = inv;
 }
 
 // Order-preserving integer of a float (NaN counts as -infinity) and back.
@@ -995,7 +1000,94 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
   }
 }
 
+// Merges a sequence's partials: CTA = 8 / W rows of one sequence (request c, row block rb, kv
+// head g), W warps a row.  The sequence holds t_seq tiles from unit s0 of the line, which is
+// cut into chunks of Z units; its piece in chunk k0 + p has slot c * spr + rb * Hkv + g + k0 + p
+// with one partial (pair) or two, q = 2 p + half: half h holds the piece's tiles of parity h
+// and exists iff the piece has more than h tiles.  o = sum 2^(m_q - M) acc_q / sum 2^(m_q - M)
+// l_q in a fixed order; a lane holds four dims, and the loads of four partials are in flight
+// together.
+template <int D, int W>
+__global__ void __launch_bounds__(256) attn_kv8_merge_tc_kernel(const AttnKv8Args a, int blocks) {
+  pdl_wait();  // the previous kernel on the stream is complete from here on
+  pdl_trigger();
+  __shared__ float s_acc[W > 1 ? 8 : 1][D];
+  __shared__ float2 s_ml[8];
+  const int Hkv = a.kv.Hkv, G = a.Hq / Hkv, R = a.K * G, spr = Hkv * a.n_rb;
+  const int wib = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = wib % W;
+  const int seq = blockIdx.x / blocks, c = seq / spr, r = seq - c * spr, rb = r / Hkv, g = r - rb * Hkv;
+  const int rr = (blockIdx.x - seq * blocks) * (8 / W) + wib / W;  // row of the block
+  const int RB = min(R, a.row_block), row = rb * a.row_block + rr;
+  const bool live = rr < a.row_block && row < R;
+  const int halves = a.pair ? 1 : 2;
+  const int* off = a.sched + 64;
+  const int Z = a.sched[2], o0 = off[c], tw = (off[c + 1] - o0) / spr;  // tw = 0: no tiles (or a bad length)
+  const int t_seq = tw - kAttn8SeqUnits, s0 = o0 + r * tw + kAttn8SeqUnits, k0 = s0 / Z;
+  const int ns = live && t_seq > 0 ? halves * ((s0 + t_seq - 1) / Z - k0 + 1) : 0;
+  const size_t base = (size_t)(seq + k0) * halves * RB + rr;
+  const bool on = lane * 4 < D;
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto fold = [&](float2 ml, float4 x) {
+    if (ml.y == 0.f) return;  // no key seen
+    const float mn = fmaxf(M, ml.x);
+    const float sc = L == 0.f ? 0.f : exp2f(M - mn), w = exp2f(ml.x - mn);
+    L = L * sc + ml.y * w;
+    o.x = o.x * sc + x.x * w, o.y = o.y * sc + x.y * w, o.z = o.z * sc + x.z * w, o.w = o.w * sc + x.w * w;
+    M = mn;
+  };
+  for (int q0 = wq; q0 < ns; q0 += 4 * W) {
+    float2 ml[4];
+    float4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int q = q0 + u * W;
+      bool has = q < ns;
+      if (halves == 2 && has) {
+        const int lo = max(s0, (k0 + (q >> 1)) * Z), hi = min(s0 + t_seq, (k0 + (q >> 1) + 1) * Z);
+        has = hi - lo > (q & 1);
+      }
+      const size_t b = base + (size_t)q * RB;
+      ml[u] = has ? *(const float2*)(a.ws_ml + b * 2) : make_float2(-INFINITY, 0.f);
+      x[u] = has && on ? *(const float4*)(a.ws_acc + b * D + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) fold(ml[u], x[u]);
+  }
+  if constexpr (W > 1) {
+    if (on) *(float4*)&s_acc[wib][lane * 4] = o;
+    if (lane == 0) s_ml[wib] = make_float2(M, L);
+    __syncthreads();
+    if (wq != 0) return;
+    for (int w = 1; w < W; ++w) fold(s_ml[wib + w], on ? *(const float4*)&s_acc[wib + w][lane * 4] : o);
+  }
+  if (!live || !on) return;
+  const int j = row / G;
+  bf16* out = (bf16*)a.out + (size_t)(c * a.K + j) * a.o_rs + (size_t)(g * G + row - j * G) * D + lane * 4;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const __nv_bfloat162 y = __floats2bfloat162_rn(o.x * inv, o.y * inv), z = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  *(uint2*)out = make_uint2(*reinterpret_cast<const uint32_t*>(&y), *reinterpret_cast<const uint32_t*>(&z));
+}
+
 // ------------------------------------------------------------------ host side
+
+template <int D, int W>
+void launch_merge_w(const AttnKv8Args& a, cudaStream_t s) {
+  const int R = a.K * (a.Hq / a.kv.Hkv), rows = R < a.row_block ? R : a.row_block;
+  const int blocks = cdiv(rows, 8 / W);
+  launch_pdl_on(attn_kv8_merge_tc_kernel<D, W>, (unsigned)(a.C * a.kv.Hkv * a.n_rb * blocks), 256, 0, s, a, blocks);
+  note_launch();
+}
+
+template <int D>
+void launch_merge(const AttnKv8Args& a, cudaStream_t s) {
+  // warps per output row: enough warps in all for about 32 per SM
+  const long rows = (long)a.C * a.K * a.Hq;
+  if (rows >= 148L * 32) launch_merge_w<D, 1>(a, s);
+  else if (rows * 2 >= 148L * 32) launch_merge_w<D, 2>(a, s);
+  else if (rows * 4 >= 148L * 32) launch_merge_w<D, 4>(a, s);
+  else launch_merge_w<D, 8>(a, s);
+}
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -1043,7 +1135,7 @@ bool launch(const AttnKv8Args& a, int grid, cudaStream_t s) {
     return false;
   }
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
-  launch_pdl(kernel, grid, Warps<NR>::THREADS, L::SMEM, s, maps, a, scale_log2, box_shift);
+  launch_pdl_on(kernel, grid, Warps<NR>::THREADS, L::SMEM, s, maps, a, scale_log2, box_shift);
   note_launch();
   return true;
 }
@@ -1055,15 +1147,20 @@ bool launch_d(const AttnKv8Args& a, cudaStream_t s) {
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int grid = min(sms > 0 ? sms : 148, kMaxChunksAuto);
   const long rows = (long)a.C * a.kv.Hkv * a.n_rb * a.row_block + (a.kb ? (long)a.C * a.kv.Hkv * 2 * blk_rows(a.K) : 0);
-  launch_pdl(attn_kv8_prep_kernel<D>, 1 + (unsigned)((rows + 7) / 8), 256, 0, s, a, grid);
+  // rows a CTA in one pass; four passes once that still fills the GPU
+  const long per = 8 * (32 / (D / 8));
+  const int passes = rows >= per * 4 * 4 * sms ? 4 : 1;
+  launch_pdl(attn_kv8_prep_kernel<D>, 1 + (unsigned)((rows + per * passes - 1) / (per * passes)), 256, 0, s, a, grid,
+             passes);
   note_launch();
-  if (a.pair) return a.row_block == 96 ? launch<D, 48, true>(a, grid, s) : launch<D, 64, true>(a, grid, s);
-  switch (a.row_block) {
-    case 16: return launch<D, 16, false>(a, grid, s);
-    case 32: return launch<D, 32, false>(a, grid, s);
-    case 48: return launch<D, 48, false>(a, grid, s);
-    default: return launch<D, 64, false>(a, grid, s);
-  }
+  bool ok;
+  if (a.pair) ok = a.row_block == 96 ? launch<D, 48, true>(a, grid, s) : launch<D, 64, true>(a, grid, s);
+  else if (a.row_block == 16) ok = launch<D, 16, false>(a, grid, s);
+  else if (a.row_block == 32) ok = launch<D, 32, false>(a, grid, s);
+  else if (a.row_block == 48) ok = launch<D, 48, false>(a, grid, s);
+  else ok = launch<D, 64, false>(a, grid, s);
+  if (ok) launch_merge<D>(a, s);
+  return ok;
 }
 
 }  // namespace
@@ -1112,8 +1209,10 @@ bool attn_kv8_tc_launch(const AttnKv8Args& a, cudaStream_t s) {
     set_error("attention over the 8-bit cache: too many context tiles in one call");
     return false;
   }
-  if ((double)a.kv.num_pages * a.kv.Hkv > 2147483647.0) {
-    set_error("attention over the 8-bit cache: pool too large");
+  const double rows = (double)a.C * a.kv.Hkv * (a.n_rb * a.row_block + 2.0 * blk_rows(a.K));
+  if ((double)a.kv.num_pages * a.kv.Hkv > 2147483647.0 || rows > 2147483647.0 ||
+      (double)a.C * a.K * a.Hq > 2147483647.0) {
+    set_error("attention over the 8-bit cache: pool or batch too large");
     return false;
   }
   return a.kv.D == 128 ? launch_d<128>(a, s) : launch_d<64>(a, s);

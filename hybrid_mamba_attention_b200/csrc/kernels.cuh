@@ -210,7 +210,6 @@ struct AttnKv8Args {
   float* ws_acc; float* ws_ml; // partials
   // tensor-core path (attn_kv8_tc.cu); the query rows of a kv head in n_rb blocks of
   // row_block rows
-  bool tc;
   bool pair;                   // the two halves of a block's rows share every tile: one partial a piece, else two
   int row_block, n_rb;
   int max_chunks, chunk_units; // bound of the partition's chunks; requested chunk length (0: one per SM)
