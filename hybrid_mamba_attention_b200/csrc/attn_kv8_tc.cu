@@ -456,9 +456,9 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
     // Every producer warp walks the same pieces and passes the same barriers: the loop
     // ends only at one, when the work is done or a producer has given up waiting.
     bool stopped = false;
-    Piece next = advance();
-    int next_ids = next.n > 0 ? window(next, 0) : 0;
-    for (int seq = 0;; ++seq) {
+    Piece next = {0, 0, 0, 0, 1, 0};  // (seq = -1: nothing but the look-ahead)
+    int next_ids = 0;
+    for (int seq = -1;; ++seq) {
       if (tc::bar_or<1, 32 * NPW>(!ok)) {
         stopped = true;
         break;
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       const int qslot = seq % L::NQ, quse = seq / L::NQ;
 
       // the piece's queries into buffer `qslot` once the piece before in it is done
-      if (warp == 0) {
+      if (warp == 0 && seq >= 0) {
         if (lane == 0) {
           ok = tc::mbar_wait(&ms.q_empty[qslot], (quse & 1) ^ 1, err, lim);
           if (ok) {
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           base = page_index((pc.lt0 + local) * TT);
           if (local + 4 < n_tiles) ids_ahead = window(pc, local / 4 + 1);
         }
-        if (NPW == 2 || (tile_i & 1) == pair) {
+        if ((NPW == 2 || (tile_i & 1) == pair) && seq >= 0) {
         const int st = pc.lt0 + local;  // tile of the sequence
         const int t0 = st * TT;
         const bool block = st >= ct;
@@ -540,8 +540,10 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
         }
         __syncwarp();
         }
-        ++tile_i;
-        if (++s == NS) s = 0, s_par ^= 1;
+        if (seq >= 0) {
+          ++tile_i;
+          if (++s == NS) s = 0, s_par ^= 1;
+        }
         if (local == 0) {  // look ahead while the ring is full
           next = advance();
           next_ids = next.n > 0 ? window(next, 0) : 0;
@@ -734,11 +736,11 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           if (j0 + j < cmin) e[j] = -INFINITY;
       }
     };
-    // The key's weights 2^e, added to the sums and stored in two parts, times rv, as its row
-    // of P.  `over` becomes the largest of them.
+    // The key's weights 2^e, times `add` added to the sums, and stored in two parts, times rv,
+    // as its row of P.  `over` becomes the largest of them.
     float over = 0.f;
-    auto weigh = [&](uint32_t t_s, float ck, float rv, int cmin) {
-      const tc::F2 ck2 = tc::f2(ck, ck), rv2 = tc::f2(rv, rv);
+    auto weigh = [&](uint32_t t_s, float ck, float rv, int cmin, float add) {
+      const tc::F2 ck2 = tc::f2(ck, ck), rv2 = tc::f2(rv, rv), add2 = tc::f2(add, add);
       uint8_t* prow = sP + w * L::P_BUF + key * 128;
       float top[2] = {0.f, 0.f};
 #pragma unroll
@@ -755,7 +757,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
             const float x = tc::ex2_ftz(e[j]), y = tc::ex2_ftz(e[j + 1]);
             top[k] = fmaxf(fmaxf(top[k], x), y);
             const tc::F2 p = tc::f2(x, y);
-            l2[(j0 + j) / 2] = tc::f2_add(l2[(j0 + j) / 2], p);
+            l2[(j0 + j) / 2] = tc::f2_fma(p, add2, l2[(j0 + j) / 2]);
             float u, v;
             tc::f2_get(tc::f2_mul(p, rv2), u, v);
             ph[k] = __floats2half2_rn(u, v);
@@ -775,27 +777,6 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       }
       over = fmaxf(top[0], top[1]);
     };
-    // Takes the weights that weigh() added out of the sums again.  What a sum loses by that is
-    // 2^-24 of the weight, which is the new maximum's at most; a weight that overflowed
-    // leaves a new maximum beside which the earlier sum is nothing.
-    auto unsum = [&](uint32_t t_s, float ck, int cmin) {
-      const tc::F2 ck2 = tc::f2(ck, ck);
-#pragma unroll
-      for (int j0 = 0; j0 < NC; j0 += CH) {
-        float e[CH];
-        exponents(t_s, j0, ck2, cmin, e);
-#pragma unroll
-        for (int j = 0; j < CH; j += 2) {
-          const float x = tc::ex2_ftz(e[j]), y = tc::ex2_ftz(e[j + 1]);
-          float u, v;
-          tc::f2_get(l2[(j0 + j) / 2], u, v);
-          u = x < INFINITY ? u - x : x > 0.f ? 0.f : u;
-          v = y < INFINITY ? v - y : y > 0.f ? 0.f : v;
-          l2[(j0 + j) / 2] = tc::f2(u, v);
-        }
-      }
-    };
-
     int n = 0;  // items of the side so far
     int s = PAIR ? 0 : w;  // the item's stage
     for (;; ++n) {
@@ -827,17 +808,18 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       // kOver (or a V scale the largest so far) do the maxima move and the tile's weights
       // get computed again.  A first tile has no maxima yet.  The side's last product must be
       // done: its P buffer is free then, and O^T complete.
-      if (run && n > 0) ok = wait(&ms.pv_done[w], (n - 1) & 1);
-      if (run && ok && pend) write_partial();  // (before this item's product may overwrite it)
+      if (ok && n > 0) ok = wait(&ms.pv_done[w], (n - 1) & 1);
+      if (ok && pend) write_partial();  // (before this item's product may overwrite it)
       bool fresh = first, moved = false, leave = false;
       while (true) {
-        if (run && ok && !fresh) weigh(t_s, ck, sv * inv_mv * kPScale, cmin);
+        // (after a move the sums hold the tile's weights already: under the old maxima, and
+        // alpha has brought them to the new ones)
+        if (run && ok && !fresh) weigh(t_s, ck, sv * inv_mv * kPScale, cmin, moved && !first ? 0.f : 1.f);
         if (!group_or(!run || !ok || fresh || (!moved && (over > kOver || sv > Mv)))) break;
         // The maxima move (or the group leaves).
         const float* cq = (const float*)(sQ + (m.flags & kQSlot ? L::Q_BUF : 0) + 2 * L::ROWS * D) +
                           (PAIR ? w * NR : 0) + c0;  // the queries' scales (in place during a first tile)
         if (run && ok) {
-          if (!fresh) unsum(t_s, ck, cmin);
 #pragma unroll 1
           for (int j0 = 0; j0 < NC; j0 += 8) {
             float v[8];
@@ -877,7 +859,11 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           for (int j = 0; j < NC / 2; ++j) l2[j] = 0;
         } else {
 #pragma unroll
-          for (int j = 0; j < NC / 2; ++j) l2[j] = tc::f2_mul(l2[j], *(const tc::F2*)&alpha[2 * j]);
+          for (int j = 0; j < NC / 2; ++j) {
+            float x, y;
+            tc::f2_get(l2[j], x, y);
+            l2[j] = tc::f2(x == INFINITY ? x : x * alpha[2 * j], y == INFINITY ? y : y * alpha[2 * j + 1]);
+          }
           // O^T holds the side's earlier tiles of the piece
           tc::tc_fence_after();
 #pragma unroll 1
@@ -897,6 +883,32 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
         fresh = false, moved = true;
       }
       if (leave) break;
+      if (moved && !first) {
+        // a weight that overflowed under the old maximum is what its sum comes to now
+        bool lost = false;
+#pragma unroll
+        for (int j = 0; j < NC / 2; ++j) {
+          float x, y;
+          tc::f2_get(l2[j], x, y);
+          lost = lost || x == INFINITY || y == INFINITY;
+        }
+        if (__any_sync(0xffffffffu, lost)) {
+          const tc::F2 ck2 = tc::f2(ck, ck);
+#pragma unroll
+          for (int j0 = 0; j0 < NC; j0 += CH) {
+            float e[CH];
+            exponents(t_s, j0, ck2, cmin, e);
+#pragma unroll
+            for (int j = 0; j < CH; j += 2) {
+              float x, y;
+              tc::f2_get(l2[(j0 + j) / 2], x, y);
+              if (x == INFINITY) x = tc::ex2_ftz(e[j]);
+              if (y == INFINITY) y = tc::ex2_ftz(e[j + 1]);
+              l2[(j0 + j) / 2] = tc::f2(x, y);
+            }
+          }
+        }
+      }
       // From here on nothing waits: the item is complete.
       // S is read
       tc::tc_fence_before();
@@ -990,7 +1002,6 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       s += PAIR ? 1 : 2;
       if (s >= NS) s -= NS;
     }
-    if (ok && pend && wait(&ms.pv_done[w], (n - 1) & 1)) write_partial();  // the last piece's
     tc::tc_fence_before();
   }
   __syncthreads();

@@ -250,6 +250,22 @@ def test_attention_small_and_large_queries(H, cuda, scale):
     check_attention(H, cuda, [600, 45], 4, 8, 2, 128, 16, torch.bfloat16, True, False, scale=scale)
 
 
+def test_attention_maxima_that_jump(H, cuda):
+    # the scores' scale grows from tile to tile by steps of 2^0 .. 2^9: maxima that creep, and
+    # jumps by far more than a weight's range (a weight under the old maximum overflows)
+    lens, K, Hq, Hkv, D, page = [1300, 700], 4, 8, 2, 128, 16
+    cache = U.make_cache(lens, Hkv, D, page, 21)
+    for r, n in enumerate(lens):
+        for i in range((n + page - 1) // page):
+            cache["k_scales"][int(cache["page_table"][r, i])] = 2.0 ** (-14 + (i // 8) * (r + 1))
+    q = randn((2, K, Hq, D), 1, torch.bfloat16)
+    ref, A, S = U.attention(q, cache, lens, None, None, False)
+    out = attend(H, cfg(H, Hq, Hkv, D, page), q.to(cuda), U.to_device(cache, cuda), lens, None, None)
+    assert H.hspec_sync_status() == 0
+    over = (out.cpu().double() - ref).abs() / U.attention_bound(ref, A, S, torch.bfloat16, 1300, D)
+    assert float(over.nan_to_num(1e9).max()) <= 1.0
+
+
 def test_attention_foreign_scales(H, cuda):
     check_attention(H, cuda, [333, 129], 6, 8, 2, 128, 16, torch.bfloat16, True, False, pow2=False)
 
