@@ -60,7 +60,7 @@ struct Warps {
   static constexpr int NPW = NR <= 32 ? 4 : 2;     // producer warps: K's and V's, per pair
   static constexpr int SM_WARP0 = NR <= 32 ? 8 : 4;  // first softmax warp (a multiple of 4: warp % 4 is its TMEM quarter)
   static constexpr int THREADS = 32 * (SM_WARP0 + SMW);
-  static constexpr int kFewRegs = NR <= 32 ? 48 : 56, kManyRegs = NR <= 32 ? 96 : 104;
+  static constexpr int kFewRegs = 64, kManyRegs = NR <= 32 ? 88 : 104;
 };
 constexpr float kPScale = 8.f;    // 2^3: weights enter P times this
 constexpr float kOver = 32.f;     // 2^5: a weight may reach this before the maximum moves (P: 2^8 of e4m3's 448)
@@ -343,11 +343,11 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hkv = a.kv.Hkv, G = a.Hq / Hkv, R = a.K * G;
   const int RB = R < L::ROWS ? R : L::ROWS;  // rows of a partial
-  int* err = a.err;
-  const uint64_t lim = a.wait_ns ? (uint64_t)a.wait_ns : tc::kWaitLimitNs;  // pipeline waits
+  int* const err = a.err;
+  const uint64_t lim = a.wait_ns;  // pipeline waits (the launcher puts the default in)
   constexpr int QK_WARP = NPW, PV_WARP = NPW + 1;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // for a whole warp
-    return __all_sync(0xffffffffu, tc::mbar_wait_long(bar, parity, err, lim));
+    return __all_sync(0xffffffffu, tc::mbar_wait_long(bar, parity, a.err, a.wait_ns));
   };
 
   if (threadIdx.x == 0) {
@@ -700,8 +700,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
     bool ok = true;
     // the previous piece's partial, still in O^T
     bool pend = false;
-    size_t pend_base = 0;
-    int pend_rows = 0;
+    int pend_base = 0, pend_rows = 0;
     float pend_mul = 0.f;
     // O^T (every product issued into it has finished) to the workspace
     auto write_partial = [&]() {
@@ -716,7 +715,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (on && j0 + j < pend_rows)
-            a.ws_acc[(pend_base + j0 + j) * D + d] = fmaf(lo[j], 1.f / kLoScale, hi[j]) * pend_mul;
+            a.ws_acc[(size_t)(pend_base + j0 + j) * D + d] = fmaf(lo[j], 1.f / kLoScale, hi[j]) * pend_mul;
       }
       pend = false;
     };
@@ -960,8 +959,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
         // the side's part of the piece is complete: its sums now, its O^T during the next
         // item
         const int rows = min(NC, min(L::ROWS, R - m.rb * L::ROWS) - (PAIR ? w * NR : 0) - c0);
-        const size_t base =
-            (PAIR ? (size_t)m.slot * RB + w * NR : ((size_t)m.slot * 2 + (m.flags & kHalf ? 1 : 0)) * RB) + c0;
+        const int base = (PAIR ? m.slot * RB + w * NR : (m.slot * 2 + (m.flags & kHalf ? 1 : 0)) * RB) + c0;
         // l summed over the lanes: while the count is even, a lane keeps one half of the
         // columns and hands the other half to its partner
         float l[NC];
@@ -991,7 +989,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           if (j < cnt) ms.cmax[gq][quarter][cc + j] = l[j];
         group_or(false);
         if (quarter == 0 && lane < rows) {
-          float* ml = a.ws_ml + (base + lane) * 2;
+          float* ml = a.ws_ml + (size_t)(base + lane) * 2;
           ml[0] = ms.m[gq][lane];
           ml[1] = (ms.cmax[gq][0][lane] + ms.cmax[gq][1][lane]) + (ms.cmax[gq][2][lane] + ms.cmax[gq][3][lane]);
         }
@@ -1213,7 +1211,8 @@ size_t attn_kv8_tc_plan(AttnKv8Args& a, int split_req, void* ws) {
   return off;
 }
 
-bool attn_kv8_tc_launch(const AttnKv8Args& a, cudaStream_t s) {
+bool attn_kv8_tc_launch(AttnKv8Args& a, cudaStream_t s) {
+  if (a.wait_ns == 0) a.wait_ns = tc::kWaitLimitNs;
   // the line is indexed in 32 bits
   const long tiles = ((long)a.kv.max_pages * a.kv.page_size + TT - 1) / TT + 1;
   if ((double)a.C * a.kv.Hkv * a.n_rb * (tiles + kAttn8SeqUnits) >= (double)(1 << 30)) {
@@ -1222,7 +1221,8 @@ bool attn_kv8_tc_launch(const AttnKv8Args& a, cudaStream_t s) {
   }
   const double rows = (double)a.C * a.kv.Hkv * (a.n_rb * a.row_block + 2.0 * blk_rows(a.K));
   if ((double)a.kv.num_pages * a.kv.Hkv > 2147483647.0 || rows > 2147483647.0 ||
-      (double)a.C * a.K * a.Hq > 2147483647.0) {
+      (double)a.C * a.K * a.Hq > 2147483647.0 ||
+      ((double)a.C * a.kv.Hkv * a.n_rb + a.max_chunks) * 2 * a.row_block > 2147483647.0) {
     set_error("attention over the 8-bit cache: pool or batch too large");
     return false;
   }

@@ -227,7 +227,7 @@ constexpr int kAttn8SeqUnits = 4;
 bool attn_kv8_tc_shape(int dtype, int D, int page_size);
 // Workspace bytes; sets the plan's fields of `a` (and with ws != NULL its pointers).
 size_t attn_kv8_tc_plan(AttnKv8Args& a, int split_req, void* ws);
-bool attn_kv8_tc_launch(const AttnKv8Args& a, cudaStream_t s);
+bool attn_kv8_tc_launch(AttnKv8Args& a, cudaStream_t s);
 bool attn_kv8_supported(int K, int G, int D, const char** why);
 size_t attn_kv8_ws_bytes(int dtype, int C, int K, int Hq, const Kv8& kv, int split_req);
 // Fills the workspace fields and launches; false (message recorded) if it cannot.
