@@ -63,7 +63,10 @@ struct Warps {
   static constexpr int kFewRegs = 64, kManyRegs = NR <= 32 ? 88 : 104;
 };
 constexpr float kPScale = 8.f;    // 2^3: weights enter P times this
-constexpr float kOver = 32.f;     // 2^5: a weight may reach this before the maximum moves (P: 2^8 of e4m3's 448)
+constexpr float kOver = 32.f;     // 2^5: a weight may reach this before the reference rises (P: 2^8 of e4m3's 448)
+constexpr float kSlack = 3.f;     // a reference over a tile's maximum by more than 2^3 comes down to that,
+constexpr float kBelow = 60.f;    // though not below 2^-60 of the largest score so far,
+constexpr int kSettle = 32;       // after a context's first tile and every 32 items
 constexpr float kLoScale = 16.f;  // the low part of P is held times this
 constexpr int kMaxChunksAuto = 256, kMaxChunksExplicit = 2048;
 constexpr int kBlkRows = 64;      // scales of a block's rows (K <= 64)
@@ -93,7 +96,7 @@ struct Lay {
   static constexpr int P_BUF = TT * PN;                   // one byte an element
   static constexpr int OFF_Q = 2 * P_BUF;
   static constexpr int OFF_KV = OFF_Q + NQ * Q_BUF;
-  static constexpr int MISC = 5632;
+  static constexpr int MISC = 6144;
   static constexpr int ROOM = (227 * 1024 - 1024 - MISC - OFF_KV) / STAGE;
   static constexpr int NS = ROOM < 8 ? ROOM : 8;          // K/V ring stages
   static constexpr int OFF_MISC = OFF_KV + NS * STAGE;
@@ -114,6 +117,7 @@ enum : int {  // TileMeta::flags
   kMixed = 64,    // some key of the tile is hidden from some position
   kQPar = 128, kQSlot = 256,         // query buffer of the piece and the parity of its load
   kHalf = 512,    // odd tile of its piece
+  kSecond = 1024, // the same side's tile before was the context's first
 };
 struct alignas(16) TileMeta {  // written by producer warp 0 before the stage's barrier arrive
   int flags, cg, rb, slot;     // cg = request * Hkv + kv head; row block; the piece's partial slot
@@ -131,9 +135,9 @@ struct Misc {
   float scale[8][16];       // per stage: K scales of its eight 16-key groups, then V scales
   // per softmax group
   alignas(16) float cq[4][NR / 2];    // the query rows' scales
-  alignas(16) float nm[4][NR / 2];    // -maximum (0 while there is none)
+  alignas(16) float nm[4][NR / 2];    // -reference (0 while there is none)
   alignas(16) float alpha[4][NR / 2];
-  float m[4][NR / 2];
+  float m[4][NR / 2], top[4][NR / 2];  // the reference; the largest score so far
   float cmax[4][4][NR / 2]; // per warp: column maxima, later the rows' sums
   float svmax[4][4];
   uint4 v_nan[8];           // per stage: keys whose V row holds a NaN, as the groups find it
@@ -518,7 +522,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           m.flags = (local == 0 ? kFirst : 0) | (local == n_tiles - 1 ? kLast : 0) | (local < STEP ? kGroupFirst : 0) |
                     (local >= n_tiles - STEP ? kGroupLast : 0) | (block ? kBlock : 0) |
                     (joff + valid - 1 > 0 ? kMixed : 0) | (quse & 1 ? kQPar : 0) | (qslot ? kQSlot : 0) |
-                    (local & 1 ? kHalf : 0);
+                    (local & 1 ? kHalf : 0) | (pc.lt0 == 0 && local == STEP ? kSecond : 0);
           m.cg = pc.c * Hkv + g, m.rb = rb, m.slot = pc.c * spr + pc.r + pc.k, m.valid = valid, m.joff = joff;
           m.pad[0] = m.pad[1] = 0;
           ms.meta[s] = m;
@@ -776,7 +780,8 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       }
       over = fmaxf(top[0], top[1]);
     };
-    int n = 0;  // items of the side so far
+    int since = 0;  // items of the piece so far
+    int n = 0;      // items of the side so far
     int s = PAIR ? 0 : w;  // the item's stage
     for (;; ++n) {
       const int it = 2 * n + w, b = it & 3;
@@ -803,19 +808,27 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
         // columns below cmin do not see this key (row = rb ROWS + column, position row / G)
         cmin = key >= m.valid ? NC : max(m.joff + key, 0) * G - m.rb * L::ROWS - (PAIR ? w * NR : 0) - c0;
       }
-      // The weights are computed under the maxima so far; only if one of them then exceeds
-      // kOver (or a V scale the largest so far) do the maxima move and the tile's weights
-      // get computed again.  A first tile has no maxima yet.  The side's last product must be
-      // done: its P buffer is free then, and O^T complete.
+      // The weights are 2^(s - reference), under the references so far; only if one exceeds
+      // kOver (or a V scale the largest so far) do the references rise to the maxima and the
+      // tile's weights get computed again.  A piece's first tile has no references yet.  After
+      // a context's first tile, and every kSettle items, a reference far over the tile's own
+      // maximum comes down: the first key of a context outweighs, as a rule, any other, and
+      // weights far below the reference have few bits in P.  The side's last product must be done: its P buffer
+      // is free then, and O^T complete.
       if (ok && n > 0) ok = wait(&ms.pv_done[w], (n - 1) & 1);
       if (ok && pend) write_partial();  // (before this item's product may overwrite it)
-      bool fresh = first, moved = false, leave = false;
+      since = first ? 0 : since + 1;
+      const bool forced = first || (m.flags & kSecond) || (since & (kSettle - 1)) == 0;
+      bool weighed = false, moved = false, leave = false;
       while (true) {
-        // (after a move the sums hold the tile's weights already: under the old maxima, and
-        // alpha has brought them to the new ones)
-        if (run && ok && !fresh) weigh(t_s, ck, sv * inv_mv * kPScale, cmin, moved && !first ? 0.f : 1.f);
-        if (!group_or(!run || !ok || fresh || (!moved && (over > kOver || sv > Mv)))) break;
-        // The maxima move (or the group leaves).
+        if (run && ok && (moved || !forced)) {
+          // (after a rise the sums hold the tile's weights already: under the old references,
+          // and alpha has brought them to the new ones)
+          weigh(t_s, ck, sv * inv_mv * kPScale, cmin, weighed ? 0.f : 1.f);
+          weighed = true;
+        }
+        if (!group_or(!run || !ok || (!moved && (forced || over > kOver || sv > Mv)))) break;
+        // The references move (or the group leaves).
         const float* cq = (const float*)(sQ + (m.flags & kQSlot ? L::Q_BUF : 0) + 2 * L::ROWS * D) +
                           (PAIR ? w * NR : 0) + c0;  // the queries' scales (in place during a first tile)
         if (run && ok) {
@@ -825,7 +838,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
             tc::tmem_ld(t_s + j0, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float x = j0 + j < cmin ? -INFINITY : v[j] * ck * (fresh ? cq[j0 + j] : cqs[j0 + j]);
+              const float x = j0 + j < cmin ? -INFINITY : v[j] * ck * (first ? cq[j0 + j] : cqs[j0 + j]);
               const int top = __reduce_max_sync(0xffffffffu, float_key(x));
               if (lane == j) ms.cmax[gq][quarter][j0 + j] = key_float(top);
             }
@@ -841,19 +854,22 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           const int j = lane;
           const float cm =
               fmaxf(fmaxf(ms.cmax[gq][0][j], ms.cmax[gq][1][j]), fmaxf(ms.cmax[gq][2][j], ms.cmax[gq][3][j]));
-          const float m_old = fresh ? -INFINITY : ms.m[gq][j], m_new = fmaxf(m_old, cm);
+          const float m_old = first ? -INFINITY : ms.m[gq][j], top = first ? cm : fmaxf(ms.top[gq][j], cm);
+          float m_new = fmaxf(m_old, cm);
+          if (forced && cm > -INFINITY) m_new = fmaxf(fmaxf(cm, fminf(m_old, cm + kSlack)), top - kBelow);
           ms.m[gq][j] = m_new;
-          if (fresh) cqs[j] = cq[j];
+          ms.top[gq][j] = top;
+          if (first) cqs[j] = cq[j];
           nms[j] = m_new == -INFINITY ? 0.f : -m_new;
           alpha[j] = m_old == -INFINITY ? 1.f : exp2f(m_old - m_new);
         }
         const float sv_top = fmaxf(fmaxf(ms.svmax[gq][0], ms.svmax[gq][1]), fmaxf(ms.svmax[gq][2], ms.svmax[gq][3]));
-        const float mv_new = fresh ? sv_top : fmaxf(Mv, sv_top);
+        const float mv_new = first ? sv_top : fmaxf(Mv, sv_top);
         const float mv_ratio = mv_new > 0.f ? Mv / mv_new : 0.f;
         Mv = mv_new;
         inv_mv = Mv > 0.f ? fminf(1.f / Mv, 3.402823466e38f) : 0.f;
         group_or(false);  // cq, nm, m and alpha are written
-        if (fresh) {
+        if (first) {
 #pragma unroll
           for (int j = 0; j < NC / 2; ++j) l2[j] = 0;
         } else {
@@ -879,11 +895,11 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
             tc::tmem_st8(t_lo + j0, p);
           }
         }
-        fresh = false, moved = true;
+        moved = true;
       }
       if (leave) break;
-      if (moved && !first) {
-        // a weight that overflowed under the old maximum is what its sum comes to now
+      if (moved && !forced) {
+        // a weight that overflowed under the old reference is what its sum comes to now
         bool lost = false;
 #pragma unroll
         for (int j = 0; j < NC / 2; ++j) {

@@ -266,6 +266,28 @@ def test_attention_maxima_that_jump(H, cuda):
     assert float(over.nan_to_num(1e9).max()) <= 1.0
 
 
+@pytest.mark.parametrize("K,first", [(1, 0), (20, 0), (1, 4000)])
+def test_attention_one_key_against_many(H, cuda, K, first):
+    # one key (a context's first, or one within) holds half of the weight and some 24000 others,
+    # each 2^-14 or less of it, share the rest with values of one sign: what is lost of small
+    # weights, or of their sum, shows
+    n, Hq, Hkv, D, page = 24000, 4, 1, 128, 16
+    cache = U.make_cache([n], Hkv, D, page, 3)
+    cache["k_scales"][:] = 2.0 ** -12  # scores near zero
+    cache["v_codes"] &= 0x7F           # values >= 0
+    q = torch.ones(1, K, Hq, D).to(torch.bfloat16)
+    p, slot = int(cache["page_table"][0, first // page]), first % page
+    cache["k_codes"][p, 0, slot] = 0x7E  # 448 * 2^-12 in every dim
+    s = 448 * 2.0 ** -12 * 128 / 128 ** 0.5  # its score
+    q = q * (14.6 * 0.6931 / s)
+    ref, A, S = U.attention(q, cache, [n], None, None, False)
+    out = attend(H, cfg(H, Hq, Hkv, D, page), q.to(cuda), U.to_device(cache, cuda), [n], None, None)
+    assert H.hspec_sync_status() == 0
+    # (the sums' 2^-24 a key of the general bound, 24000 of them, is below 2^-9 of A)
+    over = (out.cpu().double() - ref).abs() / U.attention_bound(ref, A, S, torch.bfloat16, n, D)
+    assert float(over.nan_to_num(1e9).max()) <= 1.0
+
+
 def test_attention_foreign_scales(H, cuda):
     check_attention(H, cuda, [333, 129], 6, 8, 2, 128, 16, torch.bfloat16, True, False, pow2=False)
 
