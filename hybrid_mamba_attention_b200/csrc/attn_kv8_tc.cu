@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       // the piece's queries into buffer `qslot` once the piece before in it is done
       if (warp == 0 && seq >= 0) {
         if (lane == 0) {
-          ok = tc::mbar_wait(&ms.q_empty[qslot], (quse & 1) ^ 1, err, lim);
+          ok = tc::mbar_wait_long(&ms.q_empty[qslot], (quse & 1) ^ 1, err, lim);
           if (ok) {
             q_last = seq;
             tc::mbar_arrive_expect_tx(&ms.q_full[qslot], (uint32_t)L::Q_BYTES);
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
         if (in && !sound) flag_error(err, kErrPageOOB);
         if (!sound) pid = 0;  // keep the copy in bounds (its scales are 0 here)
         const int row = pid * Hkv + g;
-        ok = tc::mbar_wait_warp(&ms.kv_empty[s], s_par, err, lim);
+        ok = wait(&ms.kv_empty[s], s_par);
         if (!ok) break;
         uint8_t* dst = sKV + s * L::STAGE + pw * L::KV;
         if (lane >= 8 && lane < 16) {
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
     tc::bar_or<1, 32 * NPW>(false);  // (all have seen their stages' last fillings)
     // sentinel stage: no more work
     if (!stopped && pair == 0) {
-      if (tc::mbar_wait_warp(&ms.kv_empty[s], s_par, err, lim) && lane < 9) {  // as many arrivals as a tile's
+      if (wait(&ms.kv_empty[s], s_par) && lane < 9) {  // as many arrivals as a tile's
         if (threadIdx.x == 0) ms.meta[s].flags = kEnd;
         tc::mbar_arrive(&ms.kv_full[s]);
       }

@@ -364,7 +364,8 @@ struct StepPlan {
   int gcnt_sites;      // call sites with their own counter slice
 };
 
-StepPlan step_plan(const hspec_cfg* c, int C, int K, int max_pages) {
+// kv8: the attention layers read 8-bit caches.
+StepPlan step_plan(const hspec_cfg* c, int C, int K, int max_pages, bool kv8) {
   StepPlan s = {};
   const size_t M = (size_t)C * K, E = elem_bytes(c), d = c->d_model;
   const size_t HP = (size_t)c->n_ssm_heads * c->ssm_head_dim;
@@ -384,7 +385,9 @@ StepPlan step_plan(const hspec_cfg* c, int C, int K, int max_pages) {
   s.g = off, off += align256(M * gw * E);
   s.h0 = off, off += align256(ssm && !step_fuses_inject(c) ? (size_t)C * HPN * 4 : 0);
   s.attn = off;
-  if (att) {
+  if (att && kv8) {
+    off += hspec_attn_kv8_workspace_size(c, C, K, max_pages);
+  } else if (att) {
     s.ap = attn_plan(c, C, K, max_pages);
     off += s.ap.ws;
   }
@@ -740,11 +743,22 @@ void hspec_drafter_destroy(hspec_drafter* d) { delete d; }
 
 size_t hspec_step_workspace_size(const hspec_cfg* cfg, int C, int K, int max_pages) {
   if (!cfg || C < 1 || K < 1 || (has_kind(cfg, 'A') && max_pages < 1)) return 0;
-  return step_plan(cfg, C, K, max_pages > 0 ? max_pages : 1).total;
+  return step_plan(cfg, C, K, max_pages > 0 ? max_pages : 1, false).total;
 }
 
-hspec_status hspec_draft_step(hspec_drafter* dr, const hspec_step_in* in, const hspec_step_out* out,
-                              void* workspace, size_t ws_bytes, void* stream) {
+size_t hspec_step_kv8_workspace_size(const hspec_cfg* cfg, int C, int K, int max_pages) {
+  if (!cfg || C < 1 || K < 1 || K > 64 || (has_kind(cfg, 'A') && max_pages < 1)) return 0;
+  if ((long)(max_pages > 0 ? max_pages : 1) * cfg->page_size > (1L << 30)) return 0;
+  return step_plan(cfg, C, K, max_pages > 0 ? max_pages : 1, true).total;
+}
+
+}  // extern "C"
+
+namespace {
+
+// The draft step, over in->kv or, when kv8s is given, over one 8-bit cache per attention layer.
+hspec_status draft_step(hspec_drafter* dr, const hspec_step_in* in, const hspec_kv8_view* kv8s,
+                        const hspec_step_out* out, void* workspace, size_t ws_bytes, void* stream) {
   if (!dr || !in || !out) FAIL(HSPEC_ERR_INVALID_ARG, "drafter, in and out must be non-NULL");
   const hspec_cfg* c = &dr->cfg;
   const hspec_model_weights& W = dr->w;
@@ -761,16 +775,18 @@ hspec_status hspec_draft_step(hspec_drafter* dr, const hspec_step_in* in, const 
   if (att) {
     if (!in->ctx_lens) FAIL(HSPEC_ERR_INVALID_ARG, "ctx_lens is NULL");
     const char* why = "";
-    if (!attn_supported(c->dtype, K, c->n_q_heads / c->n_kv_heads, c->head_dim, &why))
+    const int G = c->n_q_heads / c->n_kv_heads;
+    if (kv8s ? !attn_kv8_supported(K, G, c->head_dim, &why) : !attn_supported(c->dtype, K, G, c->head_dim, &why))
       FAIL(HSPEC_ERR_UNSUPPORTED, "attention: %s", why);
     for (int i = 0; i < c->n_layers; ++i) {
       if (c->layer_kinds[i] != 'A') continue;
-      if ((st = validate_kv(c, &in->kv[n_att]))) return st;
-      if (in->kv[n_att].max_pages > max_pages) max_pages = in->kv[n_att].max_pages;
+      if ((st = kv8s ? validate_kv8(c, &kv8s[n_att]) : validate_kv(c, &in->kv[n_att]))) return st;
+      const int pages = kv8s ? kv8s[n_att].max_pages : in->kv[n_att].max_pages;
+      if (pages > max_pages) max_pages = pages;
       ++n_att;
     }
   }
-  const StepPlan sp = step_plan(c, C, K, max_pages);
+  const StepPlan sp = step_plan(c, C, K, max_pages, kv8s != nullptr);
   if (!workspace || ((uintptr_t)workspace & 255) || ws_bytes < sp.total)
     FAIL(HSPEC_ERR_WORKSPACE, "draft step needs a 256-byte aligned workspace of %zu bytes (got %zu)", sp.total,
          ws_bytes);
@@ -900,14 +916,23 @@ hspec_status hspec_draft_step(hspec_drafter* dr, const hspec_step_in* in, const 
         ProfScope p("rope", s);
         rope_rows(dtype, big, n_qkv, in->ctx_lens, C, K, Hq + Hkv, Dh, c->rope_theta, s);
       }
-      const hspec_kv_view* kv = &in->kv[ai++];
-      AttnPlan ap = attn_plan(c, C, K, kv->max_pages);
-      AttnArgs a = attn_args(c, ap, kv, in->ctx_lens, C, K, ws + sp.attn);
-      a.q = big, a.q_rs = n_qkv;
-      a.kb = big + (size_t)Hq * Dh * E, a.kb_rs = n_qkv;
-      a.vb = big + (size_t)(Hq + Hkv) * Dh * E, a.vb_rs = n_qkv;
-      a.out = g, a.o_rs = (long)Hq * Dh;
-      {
+      // q, block keys and values as columns of the projection's output, the output dense
+      auto rows = [&](auto& a) {
+        a.q = big, a.q_rs = n_qkv;
+        a.kb = big + (size_t)Hq * Dh * E, a.kb_rs = n_qkv;
+        a.vb = big + (size_t)(Hq + Hkv) * Dh * E, a.vb_rs = n_qkv;
+        a.out = g, a.o_rs = (long)Hq * Dh;
+      };
+      if (kv8s) {
+        AttnKv8Args a = attn_kv8_args(c, &kv8s[ai++], in->ctx_lens, C, K);
+        rows(a);
+        ProfScope p("attn_paged", s);
+        if (!attn_kv8(dtype, a, c->attn_split_tokens, ws + sp.attn, s)) return HSPEC_ERR_UNSUPPORTED;
+      } else {
+        const hspec_kv_view* kv = &in->kv[ai++];
+        AttnPlan ap = attn_plan(c, C, K, kv->max_pages);
+        AttnArgs a = attn_args(c, ap, kv, in->ctx_lens, C, K, ws + sp.attn);
+        rows(a);
         ProfScope p("attn_paged", s);
         if (!attn_paged(dtype, a, s)) return HSPEC_ERR_UNSUPPORTED;
       }
@@ -963,6 +988,21 @@ hspec_status hspec_draft_step(hspec_drafter* dr, const hspec_step_in* in, const 
   }
   if (out->hidden) cudaMemcpyAsync(out->hidden, x, (size_t)M * d * 4, cudaMemcpyDeviceToDevice, s);
   return check_launch("hspec_draft_step");
+}
+
+}  // namespace
+
+extern "C" {
+
+hspec_status hspec_draft_step(hspec_drafter* dr, const hspec_step_in* in, const hspec_step_out* out,
+                              void* workspace, size_t ws_bytes, void* stream) {
+  return draft_step(dr, in, nullptr, out, workspace, ws_bytes, stream);
+}
+
+hspec_status hspec_draft_step_kv8(hspec_drafter* dr, const hspec_step_in* in, const hspec_kv8_view* kv8,
+                                  const hspec_step_out* out, void* workspace, size_t ws_bytes, void* stream) {
+  if (!kv8) FAIL(HSPEC_ERR_INVALID_ARG, "kv8 is NULL");
+  return draft_step(dr, in, kv8, out, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -147,7 +147,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
 // The same wait, the thread suspended by the hardware for up to 10 us at a time (or
 // limit_ns, if that is less) instead of its default: fewer instructions spent on waiting.
 __device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, int* err, uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_test_wait(bar, parity)) return true;
   const uint32_t hint = limit_ns < 10000 ? (uint32_t)limit_ns : 10000u;
   const uint64_t t0 = global_ns();
   while (true) {

@@ -38,7 +38,8 @@ EXPORTS = ("hspec_inject_state", "hspec_ssd_block_scan", "hspec_attn_workspace_s
            "hspec_status_string", "hspec_last_error", "hspec_launch_count", "hspec_version",
            "hspec_profile_enable", "hspec_profile_read", "hspec_attn_paged_block_noalloc",
            "hspec_verify_workspace_size", "hspec_verify_greedy",
-           "hspec_kv8_write", "hspec_kv8_read", "hspec_attn_kv8_workspace_size", "hspec_attn_paged_block_kv8")
+           "hspec_kv8_write", "hspec_kv8_read", "hspec_attn_kv8_workspace_size", "hspec_attn_paged_block_kv8",
+           "hspec_step_kv8_workspace_size", "hspec_draft_step_kv8")
 HSPEC_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -121,6 +122,9 @@ def _load():
         "hspec_kv8_read": (I, [cfgp, ct.POINTER(hspec_kv8_view), P, P, I, I, P, P, L, V]),
         "hspec_attn_kv8_workspace_size": (Z, [cfgp, I, I, I]),
         "hspec_attn_paged_block_kv8": (I, [cfgp, P, ct.POINTER(hspec_kv8_view), P, P, P, I, I, P, P, Z, V]),
+        "hspec_step_kv8_workspace_size": (Z, [cfgp, I, I, I]),
+        "hspec_draft_step_kv8": (I, [P, ct.POINTER(hspec_step_in), ct.POINTER(hspec_kv8_view),
+                                     ct.POINTER(hspec_step_out), P, Z, V]),
         "hspec_verify_workspace_size": (Z, [cfgp, I, I]),
         "hspec_verify_greedy": (I, [cfgp, P, P, I, I, P, P, P, P, Z, V]),
     }
@@ -150,8 +154,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # (the raw handle: a Stream object costs as much as the rest of a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -253,10 +257,10 @@ def hspec_attn_paged_block_noalloc(cfg: hspec_cfg, q, kv: hspec_kv_view, ctx_len
 def _row_stride(rows, mate, D: int) -> int:
     """Elements between the rows of [T, Hkv, D] tensors (a slice of a wider projection's
     output will do), each row's heads dense."""
-    dense = rows.stride(2) == 1 and (rows.shape[1] == 1 or rows.stride(1) == D)
-    if not dense or rows.shape != mate.shape or rows.stride() != mate.stride():
+    st, shape = rows.stride(), rows.shape
+    if shape != mate.shape or st != mate.stride() or st[2] != 1 or (st[1] != D and shape[1] != 1):
         raise ValueError("k and v rows must be [T, Hkv, D] of the same strides, each row dense")
-    return int(rows.stride(0)) if rows.shape[0] > 1 else 0
+    return st[0] if shape[0] > 1 else 0
 
 
 def hspec_kv8_write(cfg: hspec_cfg, k_new, v_new, cu_new, first, kv: hspec_kv8_view, stream=None):
@@ -307,6 +311,19 @@ def hspec_draft_step(handle, step_in: hspec_step_in, step_out: hspec_step_out, w
     _check(_lib.hspec_draft_step(handle, ct.byref(step_in), ct.byref(step_out), _ptr(workspace),
                                  workspace.numel() * workspace.element_size(), _stream(stream)),
            "hspec_draft_step")
+
+
+def hspec_step_kv8_workspace_size(cfg: hspec_cfg, C: int, K: int, max_pages: int) -> int:
+    return int(_lib.hspec_step_kv8_workspace_size(ct.byref(cfg), C, K, max_pages))
+
+
+def hspec_draft_step_kv8(handle, step_in: hspec_step_in, kv8, step_out: hspec_step_out, workspace, stream=None):
+    """hspec_draft_step over 8-bit caches: kv8 is a sequence of hspec_kv8_view, one per
+    attention layer in order (step_in's own kv views are not read)."""
+    views = (hspec_kv8_view * max(len(kv8), 1))(*kv8)
+    _check(_lib.hspec_draft_step_kv8(handle, ct.byref(step_in), views, ct.byref(step_out), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), _stream(stream)),
+           "hspec_draft_step_kv8")
 
 
 def hspec_sync_status(stream=None) -> int:
@@ -382,6 +399,15 @@ class Drafter:
 
     def step(self, step_in: hspec_step_in, step_out: hspec_step_out, workspace, stream=None):
         hspec_draft_step(self.handle, step_in, step_out, workspace, stream)
+
+    def workspace_size_kv8(self, C: int, K: int, max_pages: int) -> int:
+        return hspec_step_kv8_workspace_size(self.cfg, C, K, max_pages)
+
+    def step_kv8(self, step_in: hspec_step_in, kv8_caches, step_out: hspec_step_out, workspace, stream=None):
+        """step() for a target with 8-bit caches (one dict as kv8_view takes per attention layer)."""
+        if len(kv8_caches) != self.shapes.layers.count("A"):
+            raise ValueError(f"{len(kv8_caches)} caches for {self.shapes.layers.count('A')} attention layers")
+        hspec_draft_step_kv8(self.handle, step_in, [kv8_view(c) for c in kv8_caches], step_out, workspace, stream)
 
     def close(self):
         if self.handle:

@@ -294,14 +294,17 @@ HSPEC_API size_t hspec_attn_kv8_workspace_size(const hspec_cfg* cfg, int C, int 
  *    HSPEC_FLAG_CAUSAL_BLOCK those before position ctx_lens[c] - (K - 1) + j.  A query
  *    that sees none gives zeros.
  * Cached values enter as the exact code * scale of their page.  On the tensor-core path
- * (bf16, D = 64 or 128, page_size a multiple of 16) the softmax weights enter the
- * product with V as two e4m3 parts, at least 8 significant bits for weights from 1 down
- * to 2^-12 of a row's largest -- fewer below, and in pages whose V scale is far smaller
- * than the largest one of the request and head (a page 2^-13 of it keeps 8 bits, each
- * further factor of two takes one) -- and non-finite query, block key or block value
- * elements enter as NaN.  A NaN in the values of one of the last K tokens makes every
- * element of the rows that see it NaN.  Other shapes run on the CUDA cores in fp32
- * (head_dim <= 256, any page size, any group).
+ * (bf16, D = 64 or 128, page_size a multiple of 16):
+ *  - the softmax weights enter the product with V as two e4m3 parts, 8 significant bits for
+ *    weights down to 2^-9 of a running reference and 2^-17 of it as the error of smaller ones
+ *    (the reference is a recent maximum of the row: it leaves out a context's first
+ *    keys, and comes down again behind other keys that outweigh all around them), and fewer
+ *    where a page's V scale is far below the largest of the request and head, a bit for
+ *    each factor of two beyond 2^-9;
+ *  - an infinity or NaN among the query, block key or block value elements enters as NaN;
+ *  - a NaN in the values of one of the last K tokens, or in the block's when the flag hides
+ *    some of it, makes every element of the rows that see it NaN.
+ * Other shapes run on the CUDA cores in fp32 (head_dim <= 256, any page size, any group).
  * q, out device [C, K, Hq, D] (dtype); k_blk, v_blk device [C, K, Hkv, D] (dtype) or both
  * NULL; ctx_lens device [C] int32; all of them and the codes 16-byte aligned; workspace
  * device, >= hspec_attn_kv8_workspace_size() bytes, 256-byte aligned.  C >= 1,
@@ -377,6 +380,16 @@ HSPEC_API hspec_status hspec_verify_greedy(const hspec_cfg* cfg, const void* log
 HSPEC_API hspec_status hspec_draft_step(hspec_drafter* drafter, const hspec_step_in* in,
                               const hspec_step_out* out, void* workspace, size_t ws_bytes,
                               void* stream);
+
+/* The same step for a target whose caches are 8-bit: kv8 holds one hspec_kv8_view per
+ * attention layer, in order, and in->kv is not read.  Same shapes as hspec_draft_step, with
+ * the attention's own (hspec_attn_paged_block_kv8); the block's keys and values stay in
+ * cfg->dtype.  Workspace: hspec_step_kv8_workspace_size() bytes for the widest of the page
+ * tables. */
+HSPEC_API size_t hspec_step_kv8_workspace_size(const hspec_cfg* cfg, int C, int K, int max_pages);
+HSPEC_API hspec_status hspec_draft_step_kv8(hspec_drafter* drafter, const hspec_step_in* in,
+                                            const hspec_kv8_view* kv8, const hspec_step_out* out,
+                                            void* workspace, size_t ws_bytes, void* stream);
 
 /* --------------------------------------------------------------- status */
 

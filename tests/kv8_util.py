@@ -129,7 +129,13 @@ def write(cache, k_new, v_new, cu, first):
 
 def attention(q, cache, lens, k_blk, v_blk, causal):
     """(out, A, S): the attention in double, [C, K, Hq, D]; A = sum_t p_t |v_t|, the scale of
-    an error in the weights; S [C, K, Hq] = the largest sum_d |q_d k_d| / sqrt(D) of a seen key."""
+    an error in the weights; S [C, K, Hq] = the largest sum_d |q_d k_d| / sqrt(D) of a seen key.
+
+    For bf16, A holds 2^-9 max_d |v_td| more for each block key.  The tensor-core path takes
+    block values as two e4m3 parts of a row scaled so that its largest element lies in
+    [128, 256): hi, then the rest, whose rounding is 2^-4 of it (2^-8 of the element) or half of
+    e4m3's smallest step, 2^-10, which is 2^-17 of a largest element of 128 or more.  The
+    bound takes 2^-8 of A, so 2^-9 of that element makes up for it."""
     C, K, Hq, D = q.shape
     Hkv = cache["k_codes"].shape[1]
     out, A = torch.zeros(C, K, Hq, D, dtype=torch.float64), torch.zeros(C, K, Hq, D, dtype=torch.float64)
@@ -151,6 +157,8 @@ def attention(q, cache, lens, k_blk, v_blk, causal):
                 p = torch.softmax(qk.sum(1) / math.sqrt(D), 0)
                 out[c, j, h] = p @ vv
                 A[c, j, h] = p @ vv.abs()
+                if k_blk is not None and q.dtype == torch.bfloat16 and seen > n:
+                    A[c, j, h] += p[n:] @ (vv[n:].abs().amax(1, keepdim=True) * 2.0 ** -9)
                 S[c, j, h] = qk.abs().sum(1).max() / math.sqrt(D)
     return out, A, S
 

@@ -422,3 +422,109 @@ def test_write_attend_verify_in_a_row(H, cuda):
         assert H.hspec_sync_status() == 0
         assert torch.equal(o1, e1) and torch.equal(o2, e2)
         assert_same_cache(dev, w2)
+
+
+# ------------------------------------------------------------------- the calls' manners
+
+def test_outputs_stay_inside(H, cuda):
+    # a read's rows and an attention's output between guards; every byte of a pool that the
+    # write has no business with keeps its value
+    Hkv, D, page, lens = 2, 128, 16, [37, 5, 90]
+    cache = U.make_cache(lens, Hkv, D, page, 7)
+    dev, c = U.to_device(cache, cuda), cfg(H, 8, Hkv, D, page)
+    for what, shape in (("read", (sum(lens), Hkv, D)), ("attn", (3, 5, 8, D))):
+        n, g = int(torch.tensor(shape).prod()), 4096
+        bufs = [torch.full((n + 2 * g,), -7.0, dtype=torch.bfloat16, device=cuda) for _ in range(2)]
+        outs = [b[g:g + n].view(shape) for b in bufs]
+        if what == "read":
+            H.hspec_kv8_read(c, H.kv8_view(dev), i32(offsets(lens), cuda), None, *outs)
+        else:
+            size = H.hspec_attn_kv8_workspace_size(c, 3, 5, dev["page_table"].shape[1])
+            wbuf = torch.full((size + 512,), 0xA5, dtype=torch.uint8, device=cuda)
+            H.hspec_attn_paged_block_kv8(c, randn(shape, 1, torch.bfloat16).to(cuda), H.kv8_view(dev), i32(lens, cuda),
+                                         None, None, outs[0], wbuf[256:256 + size])
+            outs[1].zero_()
+            assert bool((wbuf[:256] == 0xA5).all()) and bool((wbuf[256 + size:] == 0xA5).all())
+        assert H.hspec_sync_status() == 0
+        for b, o in zip(bufs, outs):
+            assert bool((b[:g] == -7.0).all()) and bool((b[-g:] == -7.0).all()) and not bool((o == -7.0).any())
+
+
+def test_another_stream_and_two_workspaces(H, cuda):
+    # two calls in flight on two streams, each with its own workspace, and two captured graphs
+    # replayed in turn, give what each gives alone
+    Hq, Hkv, D, page = 8, 2, 128, 16
+    jobs = []
+    for i, lens in enumerate(([3000, 700], [40, 2500])):
+        dev = U.to_device(U.make_cache(lens, Hkv, D, page, i), cuda)
+        q = randn((2, 4, Hq, D), 10 + i, torch.bfloat16).to(cuda)
+        c = cfg(H, Hq, Hkv, D, page)
+        ws = H.alloc_workspace(H.hspec_attn_kv8_workspace_size(c, 2, 4, dev["page_table"].shape[1]))
+        jobs.append((c, q, H.kv8_view(dev), i32(lens, cuda), torch.empty_like(q), ws, dev))
+
+    def call(j, stream=None):
+        H.hspec_attn_paged_block_kv8(j[0], j[1], j[2], j[3], None, None, j[4], j[5], stream=stream)
+
+    want = []
+    for j in jobs:
+        call(j)
+        assert H.hspec_sync_status() == 0
+        want.append(j[4].clone())
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for j, s in zip(jobs, streams):
+            call(j, s)
+    torch.cuda.synchronize()
+    for j, x in zip(jobs, want):
+        assert torch.equal(j[4], x)
+    graphs = []
+    for j, s in zip(jobs, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            call(j)
+        graphs.append(g)
+    for _ in range(3):
+        for g, j in zip(graphs, jobs):
+            j[4].zero_()
+            g.replay()
+    assert H.hspec_sync_status() == 0
+    for j, x in zip(jobs, want):
+        assert torch.equal(j[4], x)
+
+
+def test_attention_wait_runs_out(H, cuda):
+    # a 1 ns limit, which no wait for a copy from HBM meets: the call reports the timeout, the
+    # context stays usable and the next call gives the same output as before
+    lens, Hq, Hkv, D, page = [700, 4096, 1, 3000, 0, 2500], 8, 2, 128, 16
+    dev = U.to_device(U.make_cache(lens, Hkv, D, page, 4), cuda)
+    for K in (4, 20):
+        q = randn((len(lens), K, Hq, D), 1, torch.bfloat16).to(cuda)
+        want = attend(H, cfg(H, Hq, Hkv, D, page), q, dev, lens, None, None)
+        assert H.hspec_sync_status() == 0
+        attend(H, cfg(H, Hq, Hkv, D, page, wait_limit_ns=1), q, dev, lens, None, None)
+        assert H.hspec_sync_status() == H.HSPEC_ERR_DEVICE_CHECK
+        assert int(H.hspec_last_error().split("bits 0x")[1].split()[0], 16) & 8
+        assert H.hspec_sync_status() == 0
+        got = attend(H, cfg(H, Hq, Hkv, D, page), q, dev, lens, None, None)
+        assert H.hspec_sync_status() == 0 and torch.equal(got, want)
+
+
+def test_attention_of_many_short_and_few_long(H, cuda):
+    # 300 requests of 0 .. 40 tokens; two of 30000 and 17000 over many chunks
+    g = torch.Generator().manual_seed(5)
+    short = torch.randint(0, 41, (300,), generator=g).tolist()
+    check_attention(H, cuda, short, 2, 4, 1, 128, 16, torch.bfloat16, True, True, seed=3)
+    check_attention(H, cuda, [30000, 17001], 1, 2, 1, 128, 64, torch.bfloat16, False, False, seed=4)
+
+
+def test_empty_write_and_read(H, cuda):
+    c = cfg(H, 2, 2, 64, 16)
+    dev = U.to_device(U.make_cache([20], 2, 64, 16, 1), cuda)
+    before = {n: t.clone() for n, t in dev.items()}
+    k = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=cuda)
+    H.hspec_kv8_write(c, k, k, i32([0, 0], cuda), i32([20], cuda), H.kv8_view(dev))
+    H.hspec_kv8_read(c, H.kv8_view(dev), i32([0, 0], cuda), None, k, k)
+    assert H.hspec_sync_status() == 0
+    for x in ("k_codes", "v_codes", "page_table"):
+        assert torch.equal(dev[x], before[x])

@@ -125,3 +125,69 @@ def test_plain_codes_match_the_format():
 def test_plain_scale():
     assert U.scale_of(0.0) == 0.0 and U.scale_of(448.0) == 1.0 and U.scale_of(448.5) == 2.0
     assert U.scale_of(224.0) == 0.5 and U.scale_of(2.0 ** -140) == 2.0 ** -126
+
+
+def test_every_touched_page_has_one_slot():
+    # the write's and the read's numbering of touched pages: request c owns the slots
+    # [cu[c] / page + 2c, cu[c+1] / page + 2(c + 1)), whatever its range's start
+    g = torch.Generator().manual_seed(0)
+    for _ in range(200):
+        page = int(torch.randint(1, 40, (1,), generator=g))
+        C = int(torch.randint(1, 70, (1,), generator=g))
+        n = torch.randint(0, 90, (C,), generator=g) * torch.randint(0, 2, (C,), generator=g)
+        first = torch.randint(0, 200, (C,), generator=g).tolist()
+        cu = [0] + torch.cumsum(n, 0).tolist()
+        slots = cu[-1] // page + 2 * C
+        seen = {}
+        for u in range(slots):
+            # the kernels' 32-way search
+            c, m = 0, C
+            while m > 1:
+                step = (m + 31) // 32
+                hits = sum(1 for lane in range(32)
+                           if lane * step < m and cu[c + lane * step] // page + 2 * (c + lane * step) <= u)
+                if hits == 0:
+                    c = None
+                    break
+                c, m = c + (hits - 1) * step, min(step, m - (hits - 1) * step)
+            if c is None:
+                continue
+            i, f, e = u - (cu[c] // page + 2 * c), first[c], first[c] + cu[c + 1] - cu[c]
+            if i < 0 or e == f or f // page + i > (e - 1) // page:
+                continue
+            assert (c, f // page + i) not in seen
+            seen[(c, f // page + i)] = u
+        want = {(c, p) for c in range(C) if cu[c + 1] > cu[c]
+                for p in range(first[c] // page, (first[c] + cu[c + 1] - cu[c] - 1) // page + 1)}
+        assert set(seen) == want
+
+
+def test_step_kv8_refusals(H):
+    L, n0 = H._lib, H.hspec_launch_count()
+    assert L.hspec_draft_step_kv8(None, None, None, None, None, 0, None) == H.HSPEC_ERR_INVALID_ARG
+    c = cfg(H, n_ssm_heads=4, ssm_head_dim=64, d_state=32, vocab=0)
+    assert H.hspec_step_kv8_workspace_size(c, 2, 4, 8) >= H.hspec_attn_kv8_workspace_size(c, 2, 4, 8) > 0
+    assert H.hspec_step_kv8_workspace_size(c, 2, 65, 8) == 0 and H.hspec_step_kv8_workspace_size(c, 0, 4, 8) == 0
+    h = H.hspec_drafter_create(c, weights(H))
+    si = H.hspec_step_in(C=2, K=4, x_in=256, ctx_lens=256)
+    so = H.hspec_step_out()
+    views = (H.hspec_kv8_view * 1)(view(H))
+
+    def step(v):
+        return L.hspec_draft_step_kv8(h, ct.byref(si), v, ct.byref(so), 256, 1 << 40, None)
+
+    assert step(None) == H.HSPEC_ERR_INVALID_ARG and "kv8" in H.hspec_last_error()
+    views[0] = view(H, v_codes=None)
+    assert step(views) == H.HSPEC_ERR_INVALID_ARG
+    views[0] = view(H, num_pages=0)
+    assert step(views) == H.HSPEC_ERR_PAGE_OOB
+    views[0] = view(H)
+    assert L.hspec_draft_step_kv8(h, ct.byref(si), views, ct.byref(so), 256, 256, None) == H.HSPEC_ERR_WORKSPACE
+    H.hspec_drafter_destroy(h)
+    assert H.hspec_launch_count() == n0
+
+
+def weights(H):
+    mw = H.hspec_model_weights()
+    mw.layers[0].norm = mw.layers[0].W_qkv = mw.layers[0].W_o = 256
+    return mw
