@@ -74,10 +74,11 @@ constexpr int kBlkRows = 64;      // scales of a block's rows (K <= 64)
 // Rows of a block's images: its K keys in whole 32-key steps of the product with V.
 __host__ __device__ inline int blk_rows(int K) { return (K + 31) & ~31; }
 
-// Byte offset of 16-byte chunk `ch` of row r in rows of D bytes swizzled over D-byte spans.
-template <int D>
+// Byte offset of 16-byte chunk `ch` of row r in rows of W = 128, 64 or 32 bytes, swizzled over
+// spans of that width.
+template <int W>
 __device__ __forceinline__ uint32_t swz(int r, int ch) {
-  return (uint32_t)(r * D + ((D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) << 4));
+  return (uint32_t)(r * W + ((W == 128 ? ch ^ (r & 7) : W == 64 ? ch ^ ((r >> 1) & 3) : ch ^ ((r >> 2) & 1)) << 4));
 }
 
 // Query image of a sequence: hi rows, lo rows (NR rows of D bytes each, swizzled), then
@@ -87,14 +88,14 @@ __host__ __device__ inline size_t q_img_bytes(int NR, int D) { return (size_t)NR
 template <int D, int NR, bool PAIR>
 struct Lay {
   static constexpr int ROWS = PAIR ? 2 * NR : NR;         // query rows of a sequence
-  static constexpr int PN = 128;                          // columns of O^T: hi from 0, lo from 64
+  static constexpr int PN = NR == 16 ? 32 : NR == 32 ? 64 : 128;  // columns of O^T: hi from 0, lo from PN / 2
   static constexpr int NQ = PAIR ? 1 : 2;                 // query buffers
   static constexpr int Q_BYTES = ROWS * (2 * D + 4);
   static constexpr int Q_BUF = (Q_BYTES + 1023) & ~1023;
   static constexpr int KV = TT * D;                       // one operand of a stage
   static constexpr int STAGE = 2 * KV;
   static constexpr int P_BUF = TT * PN;                   // one byte an element
-  static constexpr int OFF_Q = 2 * P_BUF;
+  static constexpr int OFF_Q = (2 * P_BUF + 1023) & ~1023;
   static constexpr int OFF_KV = OFF_Q + NQ * Q_BUF;
   static constexpr int MISC = 6144;
   static constexpr int ROOM = (227 * 1024 - 1024 - MISC - OFF_KV) / STAGE;
@@ -659,16 +660,16 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           tc::tc_fence_after();
           if (elect_one()) {
             const uint32_t d = tmem + L::O_COL(w);
-            const uint64_t p = tc::sdesc_b8<128>(tc::smem_u32(sP + w * L::P_BUF));
+            const uint64_t p = tc::sdesc_b8<PN>(tc::smem_u32(sP + w * L::P_BUF));
             const uint32_t acc0 = m.flags & kGroupFirst ? 0u : 1u;
 #pragma unroll
             for (int kk = 0; kk < TT / 32; ++kk)
-              if (kk < steps) tc::mma_e4m3(d, v0 + kk * (32 * D / 16), p + kk * (32 * 128 / 16), idesc, kk > 0 ? 1u : acc0);
+              if (kk < steps) tc::mma_e4m3(d, v0 + kk * (32 * D / 16), p + kk * (32 * PN / 16), idesc, kk > 0 ? 1u : acc0);
             if (m.flags & kBlock) {  // the low parts of V follow its high parts
               const uint64_t vl = v0 + (lo_part >> 4);
 #pragma unroll
               for (int kk = 0; kk < 2; ++kk)
-                if (kk < steps) tc::mma_e4m3(d, vl + kk * (32 * D / 16), p + kk * (32 * 128 / 16), idesc, 1u);
+                if (kk < steps) tc::mma_e4m3(d, vl + kk * (32 * D / 16), p + kk * (32 * PN / 16), idesc, 1u);
             }
             if (!PAIR || j == 1) {
               if (m.flags & kLast) tc::mbar_arrive(&ms.q_empty[m.flags & kQSlot ? 1 : 0]);
@@ -744,7 +745,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
     float over = 0.f;
     auto weigh = [&](uint32_t t_s, float ck, float rv, int cmin, float add) {
       const tc::F2 ck2 = tc::f2(ck, ck), rv2 = tc::f2(rv, rv), add2 = tc::f2(add, add);
-      uint8_t* prow = sP + w * L::P_BUF + key * 128;
+      uint8_t* prow = sP + w * L::P_BUF;
       float top[2] = {0.f, 0.f};
 #pragma unroll
       for (int j0 = 0; j0 < NC; j0 += CH) {
@@ -767,15 +768,15 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           }
           split_weights(ph[0], ph[1], hi[q], lo[q]);
         }
-        // byte c0 + j0 of the row's high half, and of its low half 64 bytes on
+        // byte c0 + j0 of the row's high half, and of its low half PN / 2 bytes on
         const int ch = (c0 + j0) / 16;
         if constexpr (CH == 16) {
-          *(uint4*)(prow + ((ch ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *(uint4*)(prow + (((4 + ch) ^ (key & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *(uint4*)(prow + swz<PN>(key, ch)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *(uint4*)(prow + swz<PN>(key, PN / 32 + ch)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         } else {
           const int in = (c0 + j0) & 8;
-          *(uint2*)(prow + ((ch ^ (key & 7)) << 4) + in) = make_uint2(hi[0], hi[1]);
-          *(uint2*)(prow + (((4 + ch) ^ (key & 7)) << 4) + in) = make_uint2(lo[0], lo[1]);
+          *(uint2*)(prow + swz<PN>(key, ch) + in) = make_uint2(hi[0], hi[1]);
+          *(uint2*)(prow + swz<PN>(key, PN / 32 + ch) + in) = make_uint2(lo[0], lo[1]);
         }
       }
       over = fmaxf(top[0], top[1]);

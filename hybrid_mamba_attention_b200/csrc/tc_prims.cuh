@@ -561,15 +561,15 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn, b
          ((uint32_t)(M >> 4) << 24);
 }
 
-// Shared-memory descriptor of a one-byte operand whose rows are ROW = 128 or 64 bytes
+// Shared-memory descriptor of a one-byte operand whose rows are ROW = 128, 64 or 32 bytes
 // stored with the swizzle of that width, 8-row groups 8 * ROW bytes apart.  K-major: a row
 // is an M (or N) index and 32 bytes of it one K step.  MN-major: a row is a K index and
 // its bytes the M (or N) elements; blocks of ROW elements are lbo_bytes apart.
 template <int ROW>
 __device__ __forceinline__ uint64_t sdesc_b8(uint32_t smem_addr, uint32_t lbo_bytes = 16) {
-  static_assert(ROW == 128 || ROW == 64, "rows of one swizzle width");
+  static_assert(ROW == 128 || ROW == 64 || ROW == 32, "rows of one swizzle width");
   return (uint64_t)((smem_addr >> 4) & 0x3FFF) | ((uint64_t)((lbo_bytes >> 4) & 0x3FFF) << 16) |
-         ((uint64_t)(ROW * 8 / 16) << 32) | ((uint64_t)1 << 46) | ((uint64_t)(ROW == 128 ? 2 : 4) << 61);
+         ((uint64_t)(ROW * 8 / 16) << 32) | ((uint64_t)1 << 46) | ((uint64_t)(ROW == 128 ? 2 : ROW == 64 ? 4 : 6) << 61);
 }
 
 }  // namespace tc
