@@ -144,21 +144,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
   }
 }
 
-// The same wait, the thread suspended by the hardware for up to 10 us at a time (or
-// limit_ns, if that is less) instead of its default: fewer instructions spent on waiting.
+// The same wait, the thread suspended by the hardware for up to 10 us at a time instead of
+// its default: fewer instructions spent on waiting.  A limit below that is kept by testing
+// alone, since the hardware may suspend a thread for longer than it is asked to.
 __device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, int* err, uint64_t limit_ns) {
+  constexpr uint32_t kHint = 10000;
   if (mbar_test_wait(bar, parity)) return true;
-  const uint32_t hint = limit_ns < 10000 ? (uint32_t)limit_ns : 10000u;
   const uint64_t t0 = global_ns();
   while (true) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(hint)
-        : "memory");
+    if (limit_ns < kHint)
+      ok = mbar_test_wait(bar, parity);
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}\n"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(kHint)
+          : "memory");
     if (ok) return true;
     if (global_ns() - t0 > limit_ns) {
       flag_error(err, kErrTimeout);
