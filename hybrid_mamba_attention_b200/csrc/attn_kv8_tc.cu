@@ -48,19 +48,24 @@ namespace hspec {
 namespace {
 
 constexpr int TT = kAttn8Tile;  // keys per tile
-constexpr int SMW = 16;         // softmax warps: four groups of four
-// Warps and registers by the width of the query side.  Up to 32 columns a producer pair's
-// instructions from tile to tile are the longest of the chain, so two pairs take turns; with
-// more columns the softmax is, and its threads need the registers that a second pair would
-// take (64 columns: 850 us with one pair, 967 with two at 128 requests of 16 positions;
-// 8 columns: 459 and 415 at 64 requests of one).  setmaxnreg moves registers inside what the
-// launch gives, THREADS * LAUNCH: 256 * 48 + 512 * 96 = 768 * 80, 128 * 56 + 512 * 104 < 640 * 96.
+// Warps and registers by the width of the query side.  Two sides take the work in turn; CG groups
+// of four warps share the columns of a side's item.
+// Up to 16 columns one group holds an item whole: its fixed instructions (tests, barriers, the
+// marks of the rows) are then paid once (64 requests of 8 columns a KV head: 356 us with one group,
+// 382 with two).  With more columns two groups hide each other's latencies (128 requests of 64
+// columns: 835 us with two, 945 with one and the registers of both; 32 columns: 296 and 309).
+// Up to 32 columns a producer pair's instructions from tile to tile are the longest of the chain,
+// so two pairs take turns; with more the softmax is, and its threads need the registers that a
+// second pair would take (the 64 columns: 850 us with one pair, 967 with two).
+// setmaxnreg moves registers inside what the launch gives, THREADS * LAUNCH: 256 * 72 + 256 * 184
+// = 512 * 128, 256 * 64 + 512 * 88 = 768 * 80, 128 * 64 + 512 * 104 = 640 * 96.
 template <int NR>
 struct Warps {
-  static constexpr int NPW = NR <= 32 ? 4 : 2;     // producer warps: K's and V's, per pair
+  static constexpr int CG = NR <= 16 ? 1 : 2;
+  static constexpr int NPW = NR <= 32 ? 4 : 2;       // producer warps: K's and V's, per pair
   static constexpr int SM_WARP0 = NR <= 32 ? 8 : 4;  // first softmax warp (a multiple of 4: warp % 4 is its TMEM quarter)
-  static constexpr int THREADS = 32 * (SM_WARP0 + SMW);
-  static constexpr int kFewRegs = 64, kManyRegs = NR <= 32 ? 88 : 104;
+  static constexpr int THREADS = 32 * (SM_WARP0 + 8 * CG);
+  static constexpr int kFewRegs = CG == 1 ? 72 : 64, kManyRegs = CG == 1 ? 184 : NR <= 32 ? 88 : 104;
 };
 constexpr float kPScale = 8.f;    // 2^3: weights enter P times this
 constexpr float kOver = 32.f;     // 2^5: a weight may reach this before the reference rises (P: 2^8 of e4m3's 448)
@@ -135,12 +140,13 @@ struct Misc {
   TileMeta meta[8];
   float scale[8][16];       // per stage: K scales of its eight 16-key groups, then V scales
   // per softmax group
-  alignas(16) float cq[4][NR / 2];    // the query rows' scales
-  alignas(16) float nm[4][NR / 2];    // -reference (0 while there is none)
-  alignas(16) float alpha[4][NR / 2];
-  float m[4][NR / 2], top[4][NR / 2];  // the reference; the largest score so far
-  float cmax[4][4][NR / 2]; // per warp: column maxima, later the rows' sums
-  float svmax[4][4];
+  static constexpr int NG = 2 * Warps<NR>::CG, NC = NR / Warps<NR>::CG;  // groups, their columns
+  alignas(16) float cq[NG][NC];       // the query rows' scales
+  alignas(16) float nm[NG][NC];       // -reference (0 while there is none)
+  alignas(16) float alpha[NG][NC];
+  float m[NG][NC], top[NG][NC];       // the reference; the largest score so far
+  float cmax[NG][4][NC];              // per warp: column maxima, later the rows' sums
+  float svmax[NG][4];
   uint4 v_nan[8];           // per stage: keys whose V row holds a NaN, as the groups find it
 };
 
@@ -333,7 +339,7 @@ template <int D, int NR, bool PAIR>
 __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
     attn_kv8_tc_kernel(const __grid_constant__ Maps maps, const AttnKv8Args a, float scale_log2, int box_shift) {
   using L = Lay<D, NR, PAIR>;
-  constexpr int NS = L::NS, PN = L::PN, NC = NR / 2;
+  constexpr int NS = L::NS, PN = L::PN, CG = Warps<NR>::CG, NC = NR / CG;
   constexpr int NPW = Warps<NR>::NPW, SM_WARP0 = Warps<NR>::SM_WARP0;
   constexpr int kFewRegs = Warps<NR>::kFewRegs, kManyRegs = Warps<NR>::kManyRegs;
   extern __shared__ uint8_t smem_raw[];
@@ -362,10 +368,10 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
     }
     for (int b = 0; b < 4; ++b) {
       tc::mbar_init(&ms.s_full[b], 2);  // the product's commit and the issuer's own arrival
-      tc::mbar_init(&ms.s_free[b], 8);
+      tc::mbar_init(&ms.s_free[b], 4 * CG);
     }
     for (int b = 0; b < 2; ++b) {
-      tc::mbar_init(&ms.p_full[b], 8);
+      tc::mbar_init(&ms.p_full[b], 4 * CG);
       tc::mbar_init(&ms.pv_done[b], 1);
       tc::mbar_init(&ms.q_full[b], 1);
       tc::mbar_init(&ms.q_empty[b], 1);
@@ -688,11 +694,11 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
     // ------------------------------------------------------------ softmax groups
-    // Groups 2 w and 2 w + 1 take the two halves of the columns of the items of side w.  The
-    // thread's key is its lane of the tile.  A wait that gave up (ok = false) is acted on only
+    // Groups CG w .. take the columns of the items of side w, NC each.  The thread's key is its
+    // lane of the tile.  A wait that gave up (ok = false) is acted on only
     // at the group's barriers, so that all four warps leave together.
-    const int gq = (warp - SM_WARP0) >> 2, w = gq >> 1, quarter = warp & 3;
-    const int c0 = (gq & 1) * NC;  // first column
+    const int gq = (warp - SM_WARP0) >> 2, w = gq / CG, quarter = warp & 3;
+    const int c0 = gq % CG * NC;  // first column
     const int key = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t t_hi = tmem + lane_off + L::O_COL(w) + c0, t_lo = t_hi + PN / 2;
@@ -851,8 +857,8 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           leave = true;
           break;
         }
-        if (quarter == 0 && lane < NC) {
-          const int j = lane;
+        if (quarter == 0)
+          for (int j = lane; j < NC; j += 32) {
           const float cm =
               fmaxf(fmaxf(ms.cmax[gq][0][j], ms.cmax[gq][1][j]), fmaxf(ms.cmax[gq][2][j], ms.cmax[gq][3][j]));
           const float m_old = first ? -INFINITY : ms.m[gq][j], top = first ? cm : fmaxf(ms.top[gq][j], cm);
@@ -1005,11 +1011,12 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
         for (int j = 0; j < NC / 2; ++j)
           if (j < cnt) ms.cmax[gq][quarter][cc + j] = l[j];
         group_or(false);
-        if (quarter == 0 && lane < rows) {
-          float* ml = a.ws_ml + (size_t)(base + lane) * 2;
-          ml[0] = ms.m[gq][lane];
-          ml[1] = (ms.cmax[gq][0][lane] + ms.cmax[gq][1][lane]) + (ms.cmax[gq][2][lane] + ms.cmax[gq][3][lane]);
-        }
+        if (quarter == 0)
+          for (int j = lane; j < rows; j += 32) {
+            float* ml = a.ws_ml + (size_t)(base + j) * 2;
+            ml[0] = ms.m[gq][j];
+            ml[1] = (ms.cmax[gq][0][j] + ms.cmax[gq][1][j]) + (ms.cmax[gq][2][j] + ms.cmax[gq][3][j]);
+          }
         group_or(false);  // cmax and m may be written again
         pend = true, pend_base = base, pend_rows = rows;
         pend_mul = Mv * (1.f / kPScale);
