@@ -27,18 +27,19 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 32;              // query rows per CTA
 constexpr int RW = kRows / kWarps;     // rows per warp
 constexpr int kTile = 32;              // keys per tile
-constexpr int kMaxDpl = 8;             // dims per lane (head_dim <= 256)
+constexpr int kKeys = kTile / kWarps;  // keys of a tile that a warp copies
 
 // Shared memory in floats: q [32][Dp], k [32][Dp + 4] (a lane per key reads float4s: the
-// four extra words put the lanes on different banks), v [32][Dp], p [8][RW][32].
+// four extra words put the lanes on different banks), v [32][Dp], p [8][32][RW].
 __host__ __device__ inline int dim_pad(int D) { return (D + 3) & ~3; }
 inline size_t split_smem(int D) {
   const int Dp = dim_pad(D);
   return (size_t)(kRows * Dp + kTile * (Dp + 4) + kTile * Dp + kRows * kTile) * sizeof(float);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) attn_kv8_split_kernel(const AttnKv8Args a, float scale_log2) {
+// E dims per lane: head_dim <= 32 E.
+template <typename T, int E>
+__global__ void __launch_bounds__(kThreads, 2) attn_kv8_split_kernel(const AttnKv8Args a, float scale_log2) {
   pdl_wait();  // the previous kernel on the stream is complete from here on
   pdl_trigger();
   extern __shared__ float4 sm4[];
@@ -61,50 +62,70 @@ __global__ void __launch_bounds__(kThreads) attn_kv8_split_kernel(const AttnKv8A
   if (t_begin >= total) return;  // the merge reads only the splits that hold tokens
   const int t_end = min(total, t_begin + a.split_tokens);
 
-  for (int i = threadIdx.x; i < kRows * Dp; i += kThreads) {
-    const int r = rb * kRows + i / Dp, e = i % Dp;
-    float v = 0.f;
-    if (r < R && e < D)
-      v = to_f(((const T*)a.q)[(size_t)(c * a.K + r / G) * a.q_rs + (size_t)(g * G + r % G) * D + e]) * scale_log2;
-    sQ[i] = v;
-  }
   // keys [0, vis) are seen by the row
   int vis[RW];
-  float m[RW], l[RW], acc[RW][kMaxDpl];
+  float m[RW], l[RW], acc[RW][E];
 #pragma unroll
   for (int r = 0; r < RW; ++r) {
     const int row = rb * kRows + warp * RW + r, j = row / G;
+    const T* q = (const T*)a.q + (size_t)(c * a.K + j) * a.q_rs + (size_t)(g * G + row % G) * D;
+    for (int e = lane; e < Dp; e += 32)  // read by this warp alone
+      sQ[(warp * RW + r) * Dp + e] = row < R && e < D ? to_f(q[e]) * scale_log2 : 0.f;
     vis[r] = row >= R ? 0 : !a.causal ? total : a.kb ? ctx + j + 1 : ctx - (a.K - 1) + j;
     m[r] = -INFINITY, l[r] = 0.f;
 #pragma unroll
-    for (int i = 0; i < kMaxDpl; ++i) acc[r][i] = 0.f;
+    for (int i = 0; i < E; ++i) acc[r][i] = 0.f;
   }
   const int32_t* table = a.kv.table + (size_t)c * a.kv.max_pages;
 
+  // Lane t of each warp looks up the page and the scales of key t0 + t, so that the copies of
+  // the codes that follow depend on nothing but registers.
+  auto look_up = [&](int t0, long& off, float& ks, float& vs) {
+    const int t = t0 + lane;
+    off = -1, ks = vs = 0.f;  // a bad page's keys read as 0
+    if (t >= min(t_end, ctx)) return;
+    const int pg = table[t / page];
+    if (pg >= 0 && pg < a.kv.num_pages) {
+      const size_t ph = (size_t)pg * Hkv + g;
+      off = (long)((ph * page + t % page) * D), ks = a.kv.ks[ph], vs = a.kv.vs[ph];
+    } else {
+      flag_error(a.err, kErrPageOOB);
+    }
+  };
+  long off, off_next;
+  float ks, vs, ks_next, vs_next;
+  look_up(t_begin, off, ks, vs);
   for (int t0 = t_begin; t0 < t_end; t0 += kTile) {
+    look_up(t0 + kTile, off_next, ks_next, vs_next);
     __syncthreads();
-    for (int i = threadIdx.x; i < kTile * Dp; i += kThreads) {
-      const int tt = i / Dp, e = i % Dp, t = t0 + tt;
-      float k = 0.f, v = 0.f;
-      if (e < D && t < t_end) {
-        if (t < ctx) {
-          const int pg = table[t / page];
-          if (pg >= 0 && pg < a.kv.num_pages) {
-            const size_t ph = (size_t)pg * Hkv + g, off = (ph * page + t % page) * D + e;
-            k = e4m3_to_f(a.kv.k[off]) * a.kv.ks[ph];
-            v = e4m3_to_f(a.kv.v[off]) * a.kv.vs[ph];
-          } else if (e == 0) {
-            flag_error(a.err, kErrPageOOB);
-          }
-        } else {
+    // a warp copies four keys, a lane the dims lane, lane + 32, ...
+    for (int e0 = 0; e0 < Dp; e0 += 32) {
+      const int e = e0 + lane;
+      float k[kKeys], v[kKeys];
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) {
+        const int tt = warp * kKeys + i, t = t0 + tt;
+        const long o = __shfl_sync(0xffffffffu, off, tt);
+        const float kscale = __shfl_sync(0xffffffffu, ks, tt), vscale = __shfl_sync(0xffffffffu, vs, tt);
+        k[i] = v[i] = 0.f;
+        if (e < D && o >= 0) {
+          k[i] = e4m3_to_f(a.kv.k[o + e]) * kscale;
+          v[i] = e4m3_to_f(a.kv.v[o + e]) * vscale;
+        } else if (e < D && t >= ctx && t < t_end) {
           const size_t row = (size_t)(c * a.K + (t - ctx));
-          k = to_f(((const T*)a.kb)[row * a.kb_rs + (size_t)g * D + e]);
-          v = to_f(((const T*)a.vb)[row * a.vb_rs + (size_t)g * D + e]);
+          k[i] = to_f(((const T*)a.kb)[row * a.kb_rs + (size_t)g * D + e]);
+          v[i] = to_f(((const T*)a.vb)[row * a.vb_rs + (size_t)g * D + e]);
         }
       }
-      sK[tt * (Dp + 4) + e] = k;
-      sV[tt * Dp + e] = v;
+      if (e < Dp) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+          sK[(warp * kKeys + i) * (Dp + 4) + e] = k[i];
+          sV[(warp * kKeys + i) * Dp + e] = v[i];
+        }
+      }
     }
+    off = off_next, ks = ks_next, vs = vs_next;
     __syncthreads();
     float s[RW];
 #pragma unroll
@@ -130,19 +151,36 @@ __global__ void __launch_bounds__(kThreads) attn_kv8_split_kernel(const AttnKv8A
       l[r] = l[r] * alpha + warp_sum(p);
       m[r] = m_new;
 #pragma unroll
-      for (int i = 0; i < kMaxDpl; ++i) acc[r][i] *= alpha;
-      sP[(warp * RW + r) * kTile + lane] = p;
+      for (int i = 0; i < E; ++i) acc[r][i] *= alpha;
+      sP[(warp * kTile + lane) * RW + r] = p;
     }
     __syncwarp();
+    // Keys that all four rows see, without a test; then those that some do.  A lane's dims from D
+    // on add up what follows in shared memory (a row's end reads at most 256 floats on, into p),
+    // and are never stored.
+    static_assert(RW == 4, "a key's weights are read as one float4");
+    const int all = min(min(nv[0], nv[1]), min(nv[2], nv[3])), any = max(max(nv[0], nv[1]), max(nv[2], nv[3]));
+    const float4* p4 = (const float4*)(sP + warp * kTile * RW);
+    const float* v1 = sV + lane;
+#pragma unroll 4
+    for (int t = 0; t < all; ++t) {
+      const float4 p = p4[t];
 #pragma unroll
-    for (int i = 0; i < kMaxDpl; ++i) {
-      const int e = lane + 32 * i;
-      if (e >= D) break;
-      for (int t = 0; t < kTile; ++t) {
-        const float v = sV[t * Dp + e];
+      for (int i = 0; i < E; ++i) {
+        const float v = v1[t * Dp + 32 * i];
+        acc[0][i] = fmaf(p.x, v, acc[0][i]);
+        acc[1][i] = fmaf(p.y, v, acc[1][i]);
+        acc[2][i] = fmaf(p.z, v, acc[2][i]);
+        acc[3][i] = fmaf(p.w, v, acc[3][i]);
+      }
+    }
+    for (int t = all; t < any; ++t) {
 #pragma unroll
-        for (int r = 0; r < RW; ++r)
-          if (t < nv[r]) acc[r][i] = fmaf(sP[(warp * RW + r) * kTile + t], v, acc[r][i]);
+      for (int r = 0; r < RW; ++r) {
+        if (t >= nv[r]) continue;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          acc[r][i] = fmaf(sP[(warp * kTile + t) * RW + r], v1[t * Dp + 32 * i], acc[r][i]);
       }
     }
   }
@@ -152,7 +190,7 @@ __global__ void __launch_bounds__(kThreads) attn_kv8_split_kernel(const AttnKv8A
     if (row >= R) break;
     const size_t base = (((size_t)c * Hkv + g) * a.n_splits + split) * R + row;
 #pragma unroll
-    for (int i = 0; i < kMaxDpl; ++i)
+    for (int i = 0; i < E; ++i)
       if (lane + 32 * i < D) a.ws_acc[base * D + lane + 32 * i] = acc[r][i];
     if (lane == 0) {
       a.ws_ml[base * 2] = m[r];
@@ -241,19 +279,24 @@ void launch_merge(const AttnKv8Args& a, cudaStream_t s) {
   }
 }
 
-template <typename T>
-bool launch_split(const AttnKv8Args& a, cudaStream_t s) {
+template <typename T, int E>
+bool launch_split_e(const AttnKv8Args& a, cudaStream_t s) {
   const size_t smem = split_smem(a.kv.D);
-  if (cudaFuncSetAttribute(attn_kv8_split_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+  if (cudaFuncSetAttribute(attn_kv8_split_kernel<T, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess) {
     set_error("cudaFuncSetAttribute(attn_kv8_split_kernel) failed");
     return false;
   }
   const int nrb = cdiv((long)a.K * (a.Hq / a.kv.Hkv), kRows);
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)a.kv.D);
-  launch_pdl(attn_kv8_split_kernel<T>, dim3(a.n_splits, a.kv.Hkv * nrb, a.C), kThreads, smem, s, a, scale_log2);
+  launch_pdl(attn_kv8_split_kernel<T, E>, dim3(a.n_splits, a.kv.Hkv * nrb, a.C), kThreads, smem, s, a, scale_log2);
   note_launch();
   return true;
+}
+
+template <typename T>
+bool launch_split(const AttnKv8Args& a, cudaStream_t s) {
+  return a.kv.D <= 64 ? launch_split_e<T, 2>(a, s) : a.kv.D <= 128 ? launch_split_e<T, 4>(a, s) : launch_split_e<T, 8>(a, s);
 }
 
 // CUDA-core path: tokens per split (a requested length, or about 16 CTAs per SM at the

@@ -51,8 +51,8 @@ constexpr int TT = kAttn8Tile;  // keys per tile
 // Warps and registers by the width of the query side.  Two sides take the work in turn; CG groups
 // of four warps share the columns of a side's item.
 // Up to 16 columns one group holds an item whole: its fixed instructions (tests, barriers, the
-// marks of the rows) are then paid once (64 requests of 8 columns a KV head: 356 us with one group,
-// 382 with two).  With more columns two groups hide each other's latencies (128 requests of 64
+// marks of the rows) are then paid once (64 requests of 8 columns a KV head: 380 us with one group,
+// 411 with two).  With more columns two groups hide each other's latencies (128 requests of 64
 // columns: 835 us with two, 945 with one and the registers of both; 32 columns: 296 and 309).
 // Up to 32 columns a producer pair's instructions from tile to tile are the longest of the chain,
 // so two pairs take turns; with more the softmax is, and its threads need the registers that a
