@@ -12,30 +12,41 @@
 //
 // Rounding.  A bf16 query row is scaled by a power of two and held as two e4m3 parts,
 // hi + lo, which carry its 8 bits (down to 2^-17 of the row's largest element); both are
-// multiplied with K into one fp32 accumulator.  The weights p = 2^(s - m) <= 2^3 enter as
-// P = p * 2^5 * (V scale / largest V scale so far), hi = e4m3(P) and lo = e4m3(16 (P - hi))
-// side by side in one N = 2R product, O = O_hi + O_lo / 16: at least 8 bits down to 2^-12
-// of the running maximum.  Row sums use the unrounded fp32 weights.  The block's own bf16
-// keys and values are two e4m3 parts with a power-of-two scale per row, too.
+// multiplied with K into one fp32 accumulator.  The weights p = 2^(s - m) <= 2^5 enter as
+// P = p * 2^3 * (V scale / largest V scale so far), hi = e4m3(P) and lo = e4m3(16 (P - hi))
+// side by side in one N = 2R product, O = O_hi + O_lo / 16: 8 bits down to 2^-9 of the
+// reference m, an absolute 2^-17 below.  Row sums use the unrounded fp32 weights.  The
+// block's own bf16 keys and values are two e4m3 parts with a power-of-two scale per row, too.
 //
-// The running maximum m of a query is reduced across the 128 lanes only when some weight
-// would exceed 2^3 (or a V scale the largest so far): each tile, a thread looks at the
-// largest exponent of its own key over all its queries and one barrier with an OR tells
-// the group; O and the sums are then rescaled.  The first tile of a piece always does it.
+// The reference m of a query starts as the first tile's maximum.  A tile's weights are
+// computed under the references so far, then checked: only where one exceeds 2^5 (or a V
+// scale the largest so far), which one barrier with an OR tells the group, the references
+// rise to the maxima, O and the sums are rescaled and the tile is weighed again.  They come
+// down, too, at a few marked items: the first key of a context outweighs the others as a
+// rule, and weights far below the reference have few bits.
 //
 // Work partition: as the bf16 path's, the sequences (request, row block, kv head) lie end
 // to end on a line of units, kAttn8SeqUnits for a start and one per 128-key tile; the line
-// is cut into one chunk per SM, and a piece (one sequence's tiles in a chunk) writes one
-// partial for the merge kernel.  The preparation kernel sums the line and, in its other
+// is cut into one chunk per SM, and a piece (one sequence's tiles in a chunk) writes one or
+// two partials for the merge kernel.  The preparation kernel sums the line and, in its other
 // CTAs, writes the queries' and the block's two-part images in their shared-memory layout,
 // each then one bulk copy.
 //
-// Warp roles (512 threads, one CTA per SM): warps 0..3 producers (a tile's K and V pages
-// as TMA boxes of up to 128 rows, spread over the warps, and the pages' scales); warp 4
-// issues S^T, warp 5 O^T (warp 4 owns TMEM); warps 8..11 and 12..15 are two softmax groups
-// that take one half of the query columns each, so O has one accumulator.
-// Bound by HBM: 2 D bytes a key and kv head.  Every wait gives up after a time bound and
-// sets the device error word.
+// Warp roles (one persistent CTA per SM; counts in Warps<NR>): producers, a warp for K and
+// one for V (a tile's pages as TMA boxes of up to 128 rows and the pages' scales, a lane
+// each); one warp that issues S^T, one that issues O^T; softmax groups of four warps, a
+// thread per key, on two sides with an accumulator O^T each.  Up to 64 query rows the sides
+// take the tiles in turn (one side's softmax runs under the other's products, two partials a
+// piece); up to 128 rows each takes half of the rows of every tile, so that a tile's bytes
+// serve both.
+//
+// What bounds it, at 32 query and 8 KV heads of 128 dims but for the first: few columns HBM,
+// 2 D bytes a key and kv head (64 requests of 1024 .. 32768 tokens, 64 query heads, one
+// position: 380 .. 400 us, 5.6 .. 5.8 TB/s of the 6.56 that a copy reaches); with more, the
+// instructions that turn S^T into P, some 14 a weight of which six split it in two parts (128
+// requests of 512 .. 16384 tokens, 16 positions: 830 us, 2.7 TB/s; prepare 25 and merge 38 of
+// them); single requests the three kernels' latencies (512 tokens: 16 us; prepare 4, this 9,
+// merge 4).  Every wait gives up after a time bound and sets the device error word.
 #include <stdint.h>
 
 #include "../../include/hspec.h"
@@ -118,7 +129,7 @@ enum : int {  // TileMeta::flags
   kEnd = 1,       // no more work (nothing else is set)
   kFirst = 2,     // first tile of its piece
   kLast = 4,      // last tile of its piece
-  kGroupFirst = 8, kGroupLast = 16,  // of its piece's tiles that the same softmax group takes
+  kGroupFirst = 8, kGroupLast = 16,  // of its piece's tiles that the same side takes
   kBlock = 32,    // the block's own keys
   kMixed = 64,    // some key of the tile is hidden from some position
   kQPar = 128, kQSlot = 256,         // query buffer of the piece and the parity of its load
@@ -126,7 +137,7 @@ enum : int {  // TileMeta::flags
   kSecond = 1024, // the same side's tile before was the context's first
 };
 struct alignas(16) TileMeta {  // written by producer warp 0 before the stage's barrier arrive
-  int flags, cg, rb, slot;     // cg = request * Hkv + kv head; row block; the piece's partial slot
+  int flags, cg, rb, slot;     // cg = request * Hkv + kv head; row block; the piece's slot
   int valid;                   // keys in the tile
   int joff;                    // key i of the tile is seen by the positions j >= joff + i
   int pad[2];
@@ -331,8 +342,8 @@ __device__ __forceinline__ TileMeta load_meta(const TileMeta* m) {
   return r;
 }
 
-// An item is one tile's work for one softmax group: item 2 n + w is the n-th of group w.
-// PAIR = false (up to 64 query rows a sequence): the groups take the tiles in turn, item
+// An item is one tile's work for one side: item 2 n + w is the n-th of side w.
+// PAIR = false (up to 64 query rows a sequence): the sides take the tiles in turn, item
 // = tile.  PAIR = true (up to 128 rows): each takes one half of the rows of every tile,
 // tile = item / 2, so that a tile's bytes serve both halves.
 template <int D, int NR, bool PAIR>
@@ -388,11 +399,10 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
   pdl_wait();  // the previous kernel on the stream is complete from here on
   pdl_trigger();
 
-  // 512 threads launch with 128 registers each; the softmax warps take 64 of the others'
   if (warp < NPW) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     // ------------------------------------------------------------ producers
-    // Warps 0 and 1 bring K and V (of the even tiles, and warps 2 and 3 of the odd ones): lane
+    // Warps 0 and 1 bring K and V (with four, of the even tiles, warps 2 and 3 of the odd): lane
     // x < 8 the tile's box x of 2^box_shift rows (within one page each), lane 8 + i the
     // scale of its 16-key group i.  All walk the same tiles; the K warp describes its tile,
     // warp 0 also loads the queries.
@@ -503,7 +513,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           base = page_index((pc.lt0 + local) * TT);
           if (local + 4 < n_tiles) ids_ahead = window(pc, local / 4 + 1);
         }
-        if ((NPW == 2 || (tile_i & 1) == pair) && seq >= 0) {
+        if ((NPW == 2 || (tile_i & 1) == pair) && seq >= 0) {  // a tile of this warp's
         const int st = pc.lt0 + local;  // tile of the sequence
         const int t0 = st * TT;
         const bool block = st >= ct;
@@ -524,7 +534,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
         }
         if (pw == 0 && lane == 0) {
           const int joff = !a.causal ? -TT : block ? 0 : a.kb ? -TT : max(t0 - ctx + a.K, -TT);
-          constexpr int STEP = PAIR ? 1 : 2;  // tiles between those of one group
+          constexpr int STEP = PAIR ? 1 : 2;  // tiles between those of one side
           TileMeta m;
           m.flags = (local == 0 ? kFirst : 0) | (local == n_tiles - 1 ? kLast : 0) | (local < STEP ? kGroupFirst : 0) |
                     (local >= n_tiles - STEP ? kGroupLast : 0) | (block ? kBlock : 0) |
@@ -594,7 +604,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
         const int flags = load_meta(&ms.meta[s]).flags;
         const int it0 = PAIR ? 2 * i : i;
         if (flags & kEnd) {
-          // wake both groups: their next items are it0 and it0 + 1
+          // wake both sides: their next items are it0 and it0 + 1
           if (lane == 0) *(volatile int*)&ms.end_item = it0;
           __syncwarp();
           for (int it = it0; it < it0 + 2; ++it) {
@@ -695,8 +705,8 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
     // ------------------------------------------------------------ softmax groups
     // Groups CG w .. take the columns of the items of side w, NC each.  The thread's key is its
-    // lane of the tile.  A wait that gave up (ok = false) is acted on only
-    // at the group's barriers, so that all four warps leave together.
+    // TMEM lane.  A wait that gave up (ok = false) is acted on only at the group's barriers, so
+    // that all four warps leave together.
     const int gq = (warp - SM_WARP0) >> 2, w = gq / CG, quarter = warp & 3;
     const int c0 = gq % CG * NC;  // first column
     const int key = quarter * 32 + lane;
@@ -820,8 +830,8 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       // tile's weights get computed again.  A piece's first tile has no references yet.  After
       // a context's first tile, and every kSettle items, a reference far over the tile's own
       // maximum comes down: the first key of a context outweighs, as a rule, any other, and
-      // weights far below the reference have few bits in P.  The side's last product must be done: its P buffer
-      // is free then, and O^T complete.
+      // weights far below the reference have few bits in P.  The side's last product must be done:
+      // its P buffer is free then, and O^T complete.
       if (ok && n > 0) ok = wait(&ms.pv_done[w], (n - 1) & 1);
       if (ok && pend) write_partial();  // (before this item's product may overwrite it)
       since = first ? 0 : since + 1;
@@ -1206,9 +1216,10 @@ bool attn_kv8_tc_shape(int dtype, int D, int page_size) {
 
 size_t attn_kv8_tc_plan(AttnKv8Args& a, int split_req, void* ws) {
   const int D = a.kv.D, Hkv = a.kv.Hkv, R = a.K * (a.Hq / Hkv);
-  // The columns of a softmax group in 16s: the tensor time, the exponentials and the
-  // registers all go by them.  Up to 64 rows the two groups take tiles in turn; more rows
-  // are two halves of up to 64 that the groups take from every tile, in blocks of 128.
+  // The columns of a side in 16s: the tensor time, the exponentials and the registers all go
+  // by them.  Up to 64 rows the sides take the tiles in turn; more rows are two halves of up to
+  // 64 that the sides take from every tile, in blocks of 128 (64 rows as two halves of 32: 922
+  // us against 828 at 128 requests of 16 positions).
   a.pair = R > 64;
   a.n_rb = cdiv(R, 128);
   a.row_block = a.pair ? 32 * cdiv(cdiv(R, a.n_rb), 32) : 16 * cdiv(R, 16);
