@@ -715,7 +715,13 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
     float *cqs = ms.cq[gq], *nms = ms.nm[gq];
     float* alpha = ms.alpha[gq];
     auto group_or = [&](bool p) -> bool { return tc::bar_or(2 + gq, 128, p); };
-    constexpr int CH = NC % 16 == 0 ? 16 : 8;  // columns at a time
+    // rows of row block rb in the group's columns (none: <= 0)
+    auto rows_of = [&](int rb) -> int { return min(NC, min(L::ROWS, R - rb * L::ROWS) - (PAIR ? w * NR : 0) - c0); };
+    constexpr int CH = NR > 16 && NC % 16 == 0 ? 16 : 8;  // columns at a time
+    // Chunks of columns without rows are passed over where they can be a third or more of the
+    // columns (8 of 16 columns: 367 us against 379; 68 of 96: 194 and 198).  Where they are less,
+    // the test in the unrolled loop costs more than it saves (128 of 128: 372 and 354).
+    constexpr bool SKIP = NR == 16 || (PAIR && NR == 48);
     tc::F2 l2[NC / 2];  // this key lane's share of the columns' sums
     float Mv = 0.f, inv_mv = 0.f;  // largest V scale of the piece, 1 / it
     bool ok = true;
@@ -729,7 +735,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       const int d = D == 128 ? key : quarter * 16 + lane;
       const bool on = D == 128 || lane < 16;
 #pragma unroll 1
-      for (int j0 = 0; j0 < NC; j0 += 8) {
+      for (int j0 = 0; j0 < pend_rows; j0 += 8) {
         float hi[8], lo[8];
         tc::tmem_ld(t_hi + j0, hi);
         tc::tmem_ld(t_lo + j0, lo);
@@ -759,12 +765,13 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
     // The key's weights 2^e, times `add` added to the sums, and stored in two parts, times rv,
     // as its row of P.  `over` becomes the largest of them.
     float over = 0.f;
-    auto weigh = [&](uint32_t t_s, float ck, float rv, int cmin, float add) {
+    auto weigh = [&](uint32_t t_s, float ck, float rv, int cmin, int cols, float add) {
       const tc::F2 ck2 = tc::f2(ck, ck), rv2 = tc::f2(rv, rv), add2 = tc::f2(add, add);
       uint8_t* prow = sP + w * L::P_BUF;
       float top[2] = {0.f, 0.f};
 #pragma unroll
       for (int j0 = 0; j0 < NC; j0 += CH) {
+        if (j0 >= cols) break;
         float e[CH];
         exponents(t_s, j0, ck2, cmin, e);
         uint32_t hi[CH / 4], lo[CH / 4];
@@ -805,7 +812,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       if (ok) ok = wait(&ms.s_full[b], (it >> 2) & 1);
       const bool run = ok && it < *(volatile int*)&ms.end_item;
       TileMeta m = {};
-      int cmin = 0;
+      int cmin = 0, cols = NC;  // cols: the group's columns that are worked on, whole chunks
       bool first = false;
       float ck = 0.f, sv = 0.f;
       const uint32_t t_s = tmem + lane_off + L::S_COL(b) + c0;
@@ -824,6 +831,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
         ck *= scale_log2;
         // columns below cmin do not see this key (row = rb ROWS + column, position row / G)
         cmin = key >= m.valid ? NC : max(m.joff + key, 0) * G - m.rb * L::ROWS - (PAIR ? w * NR : 0) - c0;
+        cols = SKIP ? min(NC, (rows_of(m.rb) + CH - 1) & -CH) : NC;
       }
       // The weights are 2^(s - reference), under the references so far; only if one exceeds
       // kOver (or a V scale the largest so far) do the references rise to the maxima and the
@@ -841,7 +849,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
         if (run && ok && (moved || !forced)) {
           // (after a rise the sums hold the tile's weights already: under the old references,
           // and alpha has brought them to the new ones)
-          weigh(t_s, ck, sv * inv_mv * kPScale, cmin, weighed ? 0.f : 1.f);
+          weigh(t_s, ck, sv * inv_mv * kPScale, cmin, cols, weighed ? 0.f : 1.f);
           weighed = true;
         }
         if (!group_or(!run || !ok || (!moved && (forced || over > kOver || sv > Mv)))) break;
@@ -850,7 +858,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
                           (PAIR ? w * NR : 0) + c0;  // the queries' scales (in place during a first tile)
         if (run && ok) {
 #pragma unroll 1
-          for (int j0 = 0; j0 < NC; j0 += 8) {
+          for (int j0 = 0; j0 < cols; j0 += 8) {
             float v[8];
             tc::tmem_ld(t_s + j0, v);
 #pragma unroll
@@ -868,18 +876,18 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           break;
         }
         if (quarter == 0)
-          for (int j = lane; j < NC; j += 32) {
-          const float cm =
-              fmaxf(fmaxf(ms.cmax[gq][0][j], ms.cmax[gq][1][j]), fmaxf(ms.cmax[gq][2][j], ms.cmax[gq][3][j]));
-          const float m_old = first ? -INFINITY : ms.m[gq][j], top = first ? cm : fmaxf(ms.top[gq][j], cm);
-          float m_new = fmaxf(m_old, cm);
-          if (forced && cm > -INFINITY) m_new = fmaxf(fmaxf(cm, fminf(m_old, cm + kSlack)), top - kBelow);
-          ms.m[gq][j] = m_new;
-          ms.top[gq][j] = top;
-          if (first) cqs[j] = cq[j];
-          nms[j] = m_new == -INFINITY ? 0.f : -m_new;
-          alpha[j] = m_old == -INFINITY ? 1.f : exp2f(m_old - m_new);
-        }
+          for (int j = lane; j < cols; j += 32) {
+            const float cm =
+                fmaxf(fmaxf(ms.cmax[gq][0][j], ms.cmax[gq][1][j]), fmaxf(ms.cmax[gq][2][j], ms.cmax[gq][3][j]));
+            const float m_old = first ? -INFINITY : ms.m[gq][j], top = first ? cm : fmaxf(ms.top[gq][j], cm);
+            float m_new = fmaxf(m_old, cm);
+            if (forced && cm > -INFINITY) m_new = fmaxf(fmaxf(cm, fminf(m_old, cm + kSlack)), top - kBelow);
+            ms.m[gq][j] = m_new;
+            ms.top[gq][j] = top;
+            if (first) cqs[j] = cq[j];
+            nms[j] = m_new == -INFINITY ? 0.f : -m_new;
+            alpha[j] = m_old == -INFINITY ? 1.f : exp2f(m_old - m_new);
+          }
         const float sv_top = fmaxf(fmaxf(ms.svmax[gq][0], ms.svmax[gq][1]), fmaxf(ms.svmax[gq][2], ms.svmax[gq][3]));
         const float mv_new = first ? sv_top : fmaxf(Mv, sv_top);
         const float mv_ratio = mv_new > 0.f ? Mv / mv_new : 0.f;
@@ -899,7 +907,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           // O^T holds the side's earlier tiles of the piece
           tc::tc_fence_after();
 #pragma unroll 1
-          for (int j0 = 0; j0 < NC; j0 += 8) {
+          for (int j0 = 0; j0 < cols; j0 += 8) {
             float o[8], p[8];
             tc::tmem_ld(t_hi + j0, o);
             tc::tmem_ld(t_lo + j0, p);
@@ -991,7 +999,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       if (m.flags & kGroupLast) {
         // the side's part of the piece is complete: its sums now, its O^T during the next
         // item
-        const int rows = min(NC, min(L::ROWS, R - m.rb * L::ROWS) - (PAIR ? w * NR : 0) - c0);
+        const int rows = rows_of(m.rb);
         const int base = (PAIR ? m.slot * RB + w * NR : (m.slot * 2 + (m.flags & kHalf ? 1 : 0)) * RB) + c0;
         // l summed over the lanes: while the count is even, a lane keeps one half of the
         // columns and hands the other half to its partner
