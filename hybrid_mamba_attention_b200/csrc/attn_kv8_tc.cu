@@ -42,7 +42,7 @@
 //
 // What bounds it, at 32 query and 8 KV heads of 128 dims but for the first: few columns HBM,
 // 2 D bytes a key and kv head (64 requests of 1024 .. 32768 tokens, 64 query heads, one
-// position: 380 .. 400 us, 5.6 .. 5.8 TB/s of the 6.56 that a copy reaches); with more, the
+// position: 370 .. 390 us, 5.7 .. 6.0 TB/s of the 6.56 that a copy reaches); with more, the
 // instructions that turn S^T into P, some 14 a weight of which six split it in two parts (128
 // requests of 512 .. 16384 tokens, 16 positions: 830 us, 2.7 TB/s; prepare 25 and merge 38 of
 // them); single requests the three kernels' latencies (512 tokens: 16 us; prepare 4, this 9,
@@ -1051,47 +1051,57 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
   }
 }
 
-// Merges a sequence's partials: CTA = 8 / W rows of one sequence (request c, row block rb, kv
-// head g), W warps a row.  The sequence holds t_seq tiles from unit s0 of the line, which is
-// cut into chunks of Z units; its piece in chunk k0 + p has slot c * spr + rb * Hkv + g + k0 + p
-// with one partial (pair) or two, q = 2 p + half: half h holds the piece's tiles of parity h
-// and exists iff the piece has more than h tiles.  o = sum 2^(m_q - M) acc_q / sum 2^(m_q - M)
-// l_q in a fixed order; a lane holds four dims, and the loads of four partials are in flight
-// together.
+// Merges a sequence's partials: W warps share a row, or (W = 1) a warp takes U = 4 rows, of one
+// sequence (request c, row block rb, kv head g).  The sequence holds t_seq tiles from unit s0 of
+// the line, which is cut into chunks of Z units; its piece in chunk k0 + p has slot c * spr + rb *
+// Hkv + g + k0 + p with one partial (pair) or two, q = 2 p + half: half h holds the piece's tiles
+// of parity h and exists iff the piece has more than h tiles.  o = sum 2^(m_q - M) acc_q / sum
+// 2^(m_q - M) l_q in a fixed order; a lane holds four dims, and the loads of several partials
+// are in flight together.  Four rows a warp find their sequence once: 16384 rows of two partials
+// 12.7 us, 14.2 with a warp a row.
+template <int W>
+struct MergeRows {
+  static constexpr int U = W == 1 ? 4 : 1;    // rows a warp
+  static constexpr int CTA = 8 / W * U;       // rows a CTA
+};
 template <int D, int W>
 __global__ void __launch_bounds__(256) attn_kv8_merge_tc_kernel(const AttnKv8Args a, int blocks) {
   pdl_wait();  // the previous kernel on the stream is complete from here on
   pdl_trigger();
+  constexpr int U = MergeRows<W>::U, P = W == 1 ? 2 : 4;  // P partials of a row in flight
   __shared__ float s_acc[W > 1 ? 8 : 1][D];
   __shared__ float2 s_ml[8];
   const int Hkv = a.kv.Hkv, G = a.Hq / Hkv, R = a.K * G, spr = Hkv * a.n_rb;
   const int wib = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = wib % W;
   const int seq = blockIdx.x / blocks, c = seq / spr, r = seq - c * spr, rb = r / Hkv, g = r - rb * Hkv;
-  const int rr = (blockIdx.x - seq * blocks) * (8 / W) + wib / W;  // row of the block
-  const int RB = min(R, a.row_block), row = rb * a.row_block + rr;
-  const bool live = rr < a.row_block && row < R;
+  const int rr = (blockIdx.x - seq * blocks) * MergeRows<W>::CTA + wib / W * U;  // first row, of the block
+  const int RB = min(R, a.row_block), row0 = rb * a.row_block + rr;
+  const int live = min(U, min(a.row_block - rr, R - row0));  // rows there are (none: <= 0)
   const int halves = a.pair ? 1 : 2;
   const int* off = a.sched + 64;
   const int Z = a.sched[2], o0 = off[c], tw = (off[c + 1] - o0) / spr;  // tw = 0: no tiles (or a bad length)
   const int t_seq = tw - kAttn8SeqUnits, s0 = o0 + r * tw + kAttn8SeqUnits, k0 = s0 / Z;
-  const int ns = live && t_seq > 0 ? halves * ((s0 + t_seq - 1) / Z - k0 + 1) : 0;
+  const int ns = live > 0 && t_seq > 0 ? halves * ((s0 + t_seq - 1) / Z - k0 + 1) : 0;
   const size_t base = (size_t)(seq + k0) * halves * RB + rr;
   const bool on = lane * 4 < D;
-  float M = -INFINITY, L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto fold = [&](float2 ml, float4 x) {
-    if (ml.y == 0.f) return;  // no key seen
-    const float mn = fmaxf(M, ml.x);
-    const float sc = L == 0.f ? 0.f : exp2f(M - mn), w = exp2f(ml.x - mn);
-    L = L * sc + ml.y * w;
-    o.x = o.x * sc + x.x * w, o.y = o.y * sc + x.y * w, o.z = o.z * sc + x.z * w, o.w = o.w * sc + x.w * w;
-    M = mn;
-  };
-  for (int q0 = wq; q0 < ns; q0 += 4 * W) {
-    float2 ml[4];
-    float4 x[4];
+  float M[U], L[U];
+  float4 o[U];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+  for (int i = 0; i < U; ++i) M[i] = -INFINITY, L[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto fold = [&](int i, float2 ml, float4 x) {
+    if (ml.y == 0.f) return;  // no key seen
+    const float mn = fmaxf(M[i], ml.x);
+    const float sc = L[i] == 0.f ? 0.f : exp2f(M[i] - mn), w = exp2f(ml.x - mn);
+    L[i] = L[i] * sc + ml.y * w;
+    o[i].x = o[i].x * sc + x.x * w, o[i].y = o[i].y * sc + x.y * w;
+    o[i].z = o[i].z * sc + x.z * w, o[i].w = o[i].w * sc + x.w * w;
+    M[i] = mn;
+  };
+  for (int q0 = wq; q0 < ns; q0 += P * W) {
+    float2 ml[P][U];
+    float4 x[P][U];
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
       const int q = q0 + u * W;
       bool has = q < ns;
       if (halves == 2 && has) {
@@ -1099,25 +1109,36 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_tc_kernel(const AttnKv8Arg
         has = hi - lo > (q & 1);
       }
       const size_t b = base + (size_t)q * RB;
-      ml[u] = has ? *(const float2*)(a.ws_ml + b * 2) : make_float2(-INFINITY, 0.f);
-      x[u] = has && on ? *(const float4*)(a.ws_acc + b * D + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const bool there = has && i < live;
+        ml[u][i] = there ? *(const float2*)(a.ws_ml + (b + i) * 2) : make_float2(-INFINITY, 0.f);
+        x[u][i] = there && on ? *(const float4*)(a.ws_acc + (b + i) * D + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) fold(ml[u], x[u]);
+    for (int u = 0; u < P; ++u)
+#pragma unroll
+      for (int i = 0; i < U; ++i) fold(i, ml[u][i], x[u][i]);
   }
   if constexpr (W > 1) {
-    if (on) *(float4*)&s_acc[wib][lane * 4] = o;
-    if (lane == 0) s_ml[wib] = make_float2(M, L);
+    if (on) *(float4*)&s_acc[wib][lane * 4] = o[0];
+    if (lane == 0) s_ml[wib] = make_float2(M[0], L[0]);
     __syncthreads();
     if (wq != 0) return;
-    for (int w = 1; w < W; ++w) fold(s_ml[wib + w], on ? *(const float4*)&s_acc[wib + w][lane * 4] : o);
+    for (int w = 1; w < W; ++w) fold(0, s_ml[wib + w], on ? *(const float4*)&s_acc[wib + w][lane * 4] : o[0]);
   }
-  if (!live || !on) return;
-  const int j = row / G;
-  bf16* out = (bf16*)a.out + (size_t)(c * a.K + j) * a.o_rs + (size_t)(g * G + row - j * G) * D + lane * 4;
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  const __nv_bfloat162 y = __floats2bfloat162_rn(o.x * inv, o.y * inv), z = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  *(uint2*)out = make_uint2(*reinterpret_cast<const uint32_t*>(&y), *reinterpret_cast<const uint32_t*>(&z));
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if (i >= live) return;
+    const int row = row0 + i, j = row / G;
+    bf16* out = (bf16*)a.out + (size_t)(c * a.K + j) * a.o_rs + (size_t)(g * G + row - j * G) * D + lane * 4;
+    const float inv = L[i] == 0.f ? 0.f : 1.f / L[i];
+    const __nv_bfloat162 y = __floats2bfloat162_rn(o[i].x * inv, o[i].y * inv),
+                         z = __floats2bfloat162_rn(o[i].z * inv, o[i].w * inv);
+    *(uint2*)out = make_uint2(*reinterpret_cast<const uint32_t*>(&y), *reinterpret_cast<const uint32_t*>(&z));
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -1125,7 +1146,7 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_tc_kernel(const AttnKv8Arg
 template <int D, int W>
 void launch_merge_w(const AttnKv8Args& a, cudaStream_t s) {
   const int R = a.K * (a.Hq / a.kv.Hkv), rows = R < a.row_block ? R : a.row_block;
-  const int blocks = cdiv(rows, 8 / W);
+  const int blocks = cdiv(rows, MergeRows<W>::CTA);
   launch_pdl_on(attn_kv8_merge_tc_kernel<D, W>, (unsigned)(a.C * a.kv.Hkv * a.n_rb * blocks), 256, 0, s, a, blocks);
   note_launch();
 }
