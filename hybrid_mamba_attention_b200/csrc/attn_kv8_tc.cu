@@ -889,10 +889,11 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
             alpha[j] = m_old == -INFINITY ? 1.f : exp2f(m_old - m_new);
           }
         const float sv_top = fmaxf(fmaxf(ms.svmax[gq][0], ms.svmax[gq][1]), fmaxf(ms.svmax[gq][2], ms.svmax[gq][3]));
-        const float mv_new = first ? sv_top : fmaxf(Mv, sv_top);
-        const float mv_ratio = mv_new > 0.f ? Mv / mv_new : 0.f;
+        // (at least the smallest normal number: its inverse is finite)
+        const float mv_new = fmaxf(first ? sv_top : fmaxf(Mv, sv_top), 1.17549435e-38f);
+        const float mv_ratio = Mv / mv_new;
         Mv = mv_new;
-        inv_mv = Mv > 0.f ? fminf(1.f / Mv, 3.402823466e38f) : 0.f;
+        inv_mv = 1.f / Mv;
         group_or(false);  // cq, nm, m and alpha are written
         if (first) {
 #pragma unroll

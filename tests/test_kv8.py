@@ -238,6 +238,14 @@ def test_attention_f32(H, cuda, lens, K, Hq, Hkv, D, page, block, causal):
     check_attention(H, cuda, lens, K, Hq, Hkv, D, page, torch.float32, block, causal)
 
 
+@pytest.mark.parametrize("K,G", [(1, 1), (3, 3), (15, 1), (2, 12), (11, 3), (7, 6), (7, 7), (13, 5), (16, 5), (16, 6),
+                                 (33, 3), (43, 3), (50, 3)])
+def test_attention_query_rows(H, cuda, K, G):
+    # 1 .. 150 query rows a kv head: every width of the query side, filled to the last column or not
+    check_attention(H, cuda, [300, 5, 0, 140], K, 2 * G, 2, 128, 16, torch.bfloat16, True, True, seed=K)
+    check_attention(H, cuda, [300, 70], K, 2 * G, 2, 64, 32, torch.bfloat16, False, False, seed=K + 1)
+
+
 @pytest.mark.parametrize("split", [0, 64, 128, 512])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_attention_split_lengths(H, cuda, split, dtype):
@@ -290,6 +298,26 @@ def test_attention_one_key_against_many(H, cuda, K, first):
 
 def test_attention_foreign_scales(H, cuda):
     check_attention(H, cuda, [333, 129], 6, 8, 2, 128, 16, torch.bfloat16, True, False, pow2=False)
+
+
+def test_attention_smallest_scales(H, cuda):
+    # V scales below the normal range (their inverse is not finite), zero, and one normal page
+    # among them; values of 448 keep the outputs normal
+    lens, K, Hq, Hkv, D, page = [333, 40, 17], 6, 8, 2, 128, 16
+    cache = U.make_cache(lens, Hkv, D, page, 8)
+    cache["v_codes"][:] = 0x7E
+    for r, e in enumerate((2.0 ** -132, 2.0 ** -131, 0.0)):
+        cache["v_scales"][cache["page_table"][r, :(lens[r] + page - 1) // page].long()] = e
+    q = randn((3, K, Hq, D), 1, torch.bfloat16)
+    for normal in (False, True):
+        if normal:
+            cache["v_scales"][cache["page_table"][0, 20].long()] = 2.0 ** -125
+        ref, A, S = U.attention(q, cache, lens, None, None, False)
+        out = attend(H, cfg(H, Hq, Hkv, D, page), q.to(cuda), U.to_device(cache, cuda), lens, None, None)
+        assert H.hspec_sync_status() == 0
+        over = (out.cpu().double() - ref).abs() / U.attention_bound(ref, A, S, torch.bfloat16, 333, D)
+        assert float(over[:2].nan_to_num(1e9).max()) <= 1.0
+        assert bool((out[2] == 0).all())
 
 
 def test_attention_rows_without_keys_are_zero(H, cuda):
