@@ -254,6 +254,8 @@ hspec_status validate_kv8(const hspec_cfg* c, const hspec_kv8_view* kv) {
     FAIL(HSPEC_ERR_PAGE_OOB, "num_pages (%d) and max_pages (%d) must be positive", kv->num_pages, kv->max_pages);
   if ((long)kv->max_pages * c->page_size > (1L << 30))
     FAIL(HSPEC_ERR_UNSUPPORTED, "max_pages * page_size exceeds 2^30 tokens");
+  if ((long)c->page_size * c->head_dim > (1L << 30))
+    FAIL(HSPEC_ERR_UNSUPPORTED, "page_size * head_dim exceeds 2^30 codes");
   return HSPEC_OK;
 }
 

@@ -242,7 +242,7 @@ HSPEC_API hspec_status hspec_attn_paged_block_noalloc(const hspec_cfg* cfg, cons
  * powers of two the division x / scale is exact, so a code is x rounded once (to
  * nearest, ties to even), and raising a page's scale when later tokens need it only
  * re-rounds codes that leave e4m3's normal range.  The calls that read a cache take any
- * finite scales >= 0. */
+ * finite scales >= 0.  page_size * head_dim <= 2^30. */
 typedef struct hspec_kv8_view {
   void* k_codes;               /* device [num_pages, Hkv, page_size, D] e4m3, 16-byte aligned */
   void* v_codes;               /* device, the same shape                                  */

@@ -76,6 +76,20 @@ def test_write_and_read_refusals(H):
     assert H.hspec_launch_count() == n0
 
 
+def test_pages_too_large_are_refused(H):
+    # a page and head's codes are counted in 32 bits
+    L, n0, kv = H._lib, H.hspec_launch_count(), view(H, max_pages=1)
+    for page, D, ok in ((1 << 23, 128, True), ((1 << 23) + 1, 128, False), (1 << 29, 2, True), (1 << 30, 2, False)):
+        c = cfg(H, page_size=page, head_dim=D)
+        want = H.HSPEC_OK if ok else H.HSPEC_ERR_UNSUPPORTED
+        assert L.hspec_kv8_write(ct.byref(c), 256, 256, 0, 256, 256, 1, 0, ct.byref(kv), None) == want
+        assert L.hspec_kv8_read(ct.byref(c), ct.byref(kv), 256, 256, 1, 0, 256, 256, 0, None) == want
+        if not ok:
+            st = L.hspec_attn_paged_block_kv8(ct.byref(c), 256, ct.byref(kv), 256, 256, 256, 1, 1, 256, 256, 1 << 50, None)
+            assert st == want and "page_size" in H.hspec_last_error()
+    assert H.hspec_launch_count() == n0
+
+
 def test_attention_refusals(H):
     L, n0 = H._lib, H.hspec_launch_count()
     INV, UNS, WSP = H.HSPEC_ERR_INVALID_ARG, H.HSPEC_ERR_UNSUPPORTED, H.HSPEC_ERR_WORKSPACE
