@@ -105,17 +105,24 @@ template <int D, int NR, bool PAIR>
 struct Lay {
   static constexpr int ROWS = PAIR ? 2 * NR : NR;         // query rows of a sequence
   static constexpr int PN = NR == 16 ? 32 : NR == 32 ? 64 : 128;  // columns of O^T: hi from 0, lo from PN / 2
-  static constexpr int NQ = PAIR ? 1 : 2;                 // query buffers
   static constexpr int Q_BYTES = ROWS * (2 * D + 4);
   static constexpr int Q_BUF = (Q_BYTES + 1023) & ~1023;
   static constexpr int KV = TT * D;                       // one operand of a stage
   static constexpr int STAGE = 2 * KV;
   static constexpr int P_BUF = TT * PN;                   // one byte an element
   static constexpr int OFF_Q = (2 * P_BUF + 1023) & ~1023;
-  static constexpr int OFF_KV = OFF_Q + NQ * Q_BUF;
   static constexpr int MISC = 6144;
-  static constexpr int ROOM = (227 * 1024 - 1024 - MISC - OFF_KV) / STAGE;
-  static constexpr int NS = ROOM < 8 ? ROOM : 8;          // K/V ring stages
+  // K/V ring stages beside nq query buffers
+  static constexpr int stages(int nq) {
+    const int room = (227 * 1024 - 1024 - MISC - OFF_Q - nq * Q_BUF) / STAGE;
+    return room < 8 ? room : 8;
+  }
+  // Query buffers: the producers run ahead by as many pieces, which short contexts need (102
+  // requests of 65 tokens, 32 kv heads: 148 us with four, 158 with two); up to 32 rows as many, up
+  // to four, as cost no stage (more rows: two or three are alike).
+  static constexpr int NQ = PAIR ? 1 : NR > 32 ? 2 : stages(4) == stages(2) ? 4 : stages(3) == stages(2) ? 3 : 2;
+  static constexpr int NS = stages(NQ);
+  static constexpr int OFF_KV = OFF_Q + NQ * Q_BUF;
   static constexpr int OFF_MISC = OFF_KV + NS * STAGE;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
   static constexpr uint32_t TMEM_COLS = 512;
@@ -132,9 +139,10 @@ enum : int {  // TileMeta::flags
   kGroupFirst = 8, kGroupLast = 16,  // of its piece's tiles that the same side takes
   kBlock = 32,    // the block's own keys
   kMixed = 64,    // some key of the tile is hidden from some position
-  kQPar = 128, kQSlot = 256,         // query buffer of the piece and the parity of its load
-  kHalf = 512,    // odd tile of its piece
-  kSecond = 1024, // the same side's tile before was the context's first
+  kQPar = 128,    // parity of the load into the piece's query buffer,
+  kQShift = 8,    // whose number is in bits 8 and 9
+  kHalf = 1024,   // odd tile of its piece
+  kSecond = 2048, // the same side's tile before was the context's first
 };
 struct alignas(16) TileMeta {  // written by producer warp 0 before the stage's barrier arrive
   int flags, cg, rb, slot;     // cg = request * Hkv + kv head; row block; the piece's slot
@@ -145,7 +153,7 @@ struct alignas(16) TileMeta {  // written by producer warp 0 before the stage's 
 
 template <int NR>
 struct Misc {
-  uint64_t kv_full[8], kv_empty[8], s_full[4], s_free[4], p_full[2], pv_done[2], q_full[2], q_empty[2], drain[2];
+  uint64_t kv_full[8], kv_empty[8], s_full[4], s_free[4], p_full[2], pv_done[2], q_full[4], q_empty[4], drain[2];
   uint32_t tmem;
   int end_item;             // items from here on do not exist
   TileMeta meta[8];
@@ -378,14 +386,14 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       tc::mbar_init(&ms.kv_empty[s], 1);
     }
     for (int b = 0; b < 4; ++b) {
+      tc::mbar_init(&ms.q_full[b], 1);
+      tc::mbar_init(&ms.q_empty[b], 1);
       tc::mbar_init(&ms.s_full[b], 2);  // the product's commit and the issuer's own arrival
       tc::mbar_init(&ms.s_free[b], 4 * CG);
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&ms.p_full[b], 4 * CG);
       tc::mbar_init(&ms.pv_done[b], 1);
-      tc::mbar_init(&ms.q_full[b], 1);
-      tc::mbar_init(&ms.q_empty[b], 1);
       tc::mbar_init(&ms.drain[b], 1);
     }
     ms.end_item = 0x7fffffff;
@@ -538,7 +546,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           TileMeta m;
           m.flags = (local == 0 ? kFirst : 0) | (local == n_tiles - 1 ? kLast : 0) | (local < STEP ? kGroupFirst : 0) |
                     (local >= n_tiles - STEP ? kGroupLast : 0) | (block ? kBlock : 0) |
-                    (joff + valid - 1 > 0 ? kMixed : 0) | (quse & 1 ? kQPar : 0) | (qslot ? kQSlot : 0) |
+                    (joff + valid - 1 > 0 ? kMixed : 0) | (quse & 1 ? kQPar : 0) | (qslot << kQShift) |
                     (local & 1 ? kHalf : 0) | (pc.lt0 == 0 && local == STEP ? kSecond : 0);
           m.cg = pc.c * Hkv + g, m.rb = rb, m.slot = pc.c * spr + pc.r + pc.k, m.valid = valid, m.joff = joff;
           m.pad[0] = m.pad[1] = 0;
@@ -617,7 +625,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           }
           break;
         }
-        const int qslot = flags & kQSlot ? 1 : 0;
+        const int qslot = flags >> kQShift & 3;
         if ((flags & kFirst) && !wait(&ms.q_full[qslot], flags & kQPar ? 1 : 0)) break;
         bool ok = true;
         const uint64_t q0 = tc::sdesc_b8<D>(tc::smem_u32(sQ + qslot * L::Q_BUF));
@@ -688,7 +696,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
                 if (kk < steps) tc::mma_e4m3(d, vl + kk * (32 * D / 16), p + kk * (32 * PN / 16), idesc, 1u);
             }
             if (!PAIR || j == 1) {
-              if (m.flags & kLast) tc::mbar_arrive(&ms.q_empty[m.flags & kQSlot ? 1 : 0]);
+              if (m.flags & kLast) tc::mbar_arrive(&ms.q_empty[m.flags >> kQShift & 3]);
               tc::mma_commit(&ms.kv_empty[s]);
             }
             tc::mma_commit(&ms.pv_done[w]);
@@ -854,7 +862,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
         }
         if (!group_or(!run || !ok || (!moved && (forced || over > kOver || sv > Mv)))) break;
         // The references move (or the group leaves).
-        const float* cq = (const float*)(sQ + (m.flags & kQSlot ? L::Q_BUF : 0) + 2 * L::ROWS * D) +
+        const float* cq = (const float*)(sQ + (m.flags >> kQShift & 3) * L::Q_BUF + 2 * L::ROWS * D) +
                           (PAIR ? w * NR : 0) + c0;  // the queries' scales (in place during a first tile)
         if (run && ok) {
 #pragma unroll 1
@@ -955,7 +963,10 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&ms.s_free[b]);
+      // A thread walks its V row from chunk `lane` on: the lanes' rows share their banks (32 requests
+      // verifying 17 positions: 172 us, 193 with all from chunk 0 on).
       uint8_t* v_row = sKV + s * L::STAGE + L::KV + key * D;
+      auto chunk = [&](int q) -> uint4* { return (uint4*)(v_row + ((q + lane) & (D / 16 - 1)) * 16); };
       if (m.flags & kMixed) {
         // a NaN in a V row that some column does not see: the product would carry it into
         // that column, too, so the row is cleared and the columns that see it get a NaN sum.
@@ -963,8 +974,9 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
         bool bad = false;
         if (key < m.valid)
           for (int h = 0; h < (m.flags & kBlock ? 2 : 1); ++h)
+#pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
-              const uint4 x = *(const uint4*)(v_row + h * blk_rows(a.K) * D + q * 16);
+              const uint4 x = chunk(q)[h * blk_rows(a.K) * (D / 16)];
               const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int z = 0; z < 4; ++z) bad = bad || __vcmpeq4(xs[z] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
@@ -975,8 +987,9 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
         bad = bad || (*mark >> lane & 1) != 0;
         if (bad) {
           for (int h = 0; h < (m.flags & kBlock ? 2 : 1); ++h)
+#pragma unroll 1
             for (int q = 0; q < D / 16; ++q)
-              *(uint4*)(v_row + h * blk_rows(a.K) * D + q * 16) = make_uint4(0, 0, 0, 0);
+              chunk(q)[h * blk_rows(a.K) * (D / 16)] = make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int j = 0; j < NC; j += 2) {
             float x, y;
@@ -990,7 +1003,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       // V rows past the last key may hold anything (their weights are 0): clear them
       if (!(m.flags & kBlock) && key >= m.valid && key < ((m.valid + 31) & ~31)) {
 #pragma unroll 1
-        for (int q = 0; q < D / 16; ++q) *(uint4*)(v_row + q * 16) = make_uint4(0, 0, 0, 0);
+        for (int q = 0; q < D / 16; ++q) *chunk(q) = make_uint4(0, 0, 0, 0);
       }
       tc::fence_proxy_async();
       tc::tc_fence_before();
