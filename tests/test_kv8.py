@@ -246,6 +246,13 @@ def test_attention_query_rows(H, cuda, K, G):
     check_attention(H, cuda, [300, 70], K, 2 * G, 2, 64, 32, torch.bfloat16, False, False, seed=K + 1)
 
 
+@pytest.mark.parametrize("page", [80, 112, 144, 256, 1024])
+def test_attention_page_sizes(H, cuda, page):
+    # tiles that begin inside pages, pages of several tiles
+    check_attention(H, cuda, [1500, 255, 257, 1], 3, 8, 2, 128, page, torch.bfloat16, True, True, seed=page)
+    check_attention(H, cuda, [2100, 1024], 1, 8, 2, 64, page, torch.bfloat16, False, False, seed=page)
+
+
 @pytest.mark.parametrize("split", [0, 64, 128, 512])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_attention_split_lengths(H, cuda, split, dtype):
