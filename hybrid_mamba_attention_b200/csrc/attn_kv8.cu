@@ -1,11 +1,11 @@
 // Paged block attention over the 8-bit KV cache (hspec_attn_paged_block_kv8): the
 // CUDA-core split kernel for any shape, the split policy, and the merge of the partials.
 //
-// attn_kv8_split_kernel: one CTA per (split, kv head g and block of 32 query rows,
+// attn_kv8_split_kernel: one CTA per (split, kv head g and block of 32 or 64 query rows,
 // request c).  Its rows are (position j, query head g*G + i) pairs, all reading kv head
 // g.  Keys and values pass through shared memory in tiles of 32, dequantised to fp32
-// (code * scale is exact there); a warp owns four rows: lane t computes the four dot
-// products of key t, the online softmax (exp2 domain) reduces over the lanes, and for
+// (code * scale is exact there); a warp owns four rows or eight: lane t computes their dot
+// products with key t, the online softmax (exp2 domain) reduces over the lanes, and for
 // the product with V a lane owns the dims t, t + 32, ...  Hidden keys are skipped, not
 // multiplied by zero, so that a NaN in one reaches no row that does not see it.
 //
@@ -24,24 +24,29 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 32;              // query rows per CTA
-constexpr int RW = kRows / kWarps;     // rows per warp
 constexpr int kTile = 32;              // keys per tile
 constexpr int kKeys = kTile / kWarps;  // keys of a tile that a warp copies
 
-// Shared memory in floats: q [32][Dp], k [32][Dp + 4] (a lane per key reads float4s: the
+// Query rows per warp, RW: each row more shares a key's loads from shared memory, eight cost
+// registers that the widest heads have not got (8 requests of 512 .. 4096 tokens, 64 rows a kv
+// head of 128 dims: 296 us with eight, 353 with four; 36 rows of 64 dims: 186 and 196).
+__host__ __device__ inline int rows_per_warp(int R, int D) { return R > 4 * kWarps && D <= 128 ? 8 : 4; }
+inline int row_blocks(int R, int D) { return cdiv(R, kWarps * rows_per_warp(R, D)); }
+
+// Shared memory in floats: q [8 RW][Dp], k [32][Dp + 4] (a lane per key reads float4s: the
 // four extra words put the lanes on different banks), v [32][Dp], p [8][32][RW].
 __host__ __device__ inline int dim_pad(int D) { return (D + 3) & ~3; }
-inline size_t split_smem(int D) {
-  const int Dp = dim_pad(D);
-  return (size_t)(kRows * Dp + kTile * (Dp + 4) + kTile * Dp + kRows * kTile) * sizeof(float);
+inline size_t split_smem(int D, int RW) {
+  const int Dp = dim_pad(D), rows = kWarps * RW;
+  return (size_t)(rows * Dp + kTile * (Dp + 4) + kTile * Dp + rows * kTile) * sizeof(float);
 }
 
 // E dims per lane: head_dim <= 32 E.
-template <typename T, int E>
+template <typename T, int E, int RW>
 __global__ void __launch_bounds__(kThreads, 2) attn_kv8_split_kernel(const AttnKv8Args a, float scale_log2) {
   pdl_wait();  // the previous kernel on the stream is complete from here on
   pdl_trigger();
+  constexpr int kRows = kWarps * RW;
   extern __shared__ float4 sm4[];
   float* sm = (float*)sm4;
   const int D = a.kv.D, Dp = dim_pad(D), Hkv = a.kv.Hkv, page = a.kv.page_size;
@@ -155,23 +160,30 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_split_kernel(const AttnK
       sP[(warp * kTile + lane) * RW + r] = p;
     }
     __syncwarp();
-    // Keys that all four rows see, without a test; then those that some do.  A lane's dims from D
-    // on add up what follows in shared memory (a row's end reads at most 256 floats on, into p),
-    // and are never stored.
-    static_assert(RW == 4, "a key's weights are read as one float4");
-    const int all = min(min(nv[0], nv[1]), min(nv[2], nv[3])), any = max(max(nv[0], nv[1]), max(nv[2], nv[3]));
+    // Keys that all the warp's rows see, without a test; then those that some do.  A lane's dims
+    // from D on add up what follows in shared memory (a row's end reads at most 256 floats on, into
+    // p), and are never stored.
+    static_assert(RW % 4 == 0, "a key's weights are read as float4s");
+    int all = nv[0], any = nv[0];
+#pragma unroll
+    for (int r = 1; r < RW; ++r) all = min(all, nv[r]), any = max(any, nv[r]);
     const float4* p4 = (const float4*)(sP + warp * kTile * RW);
     const float* v1 = sV + lane;
 #pragma unroll 4
     for (int t = 0; t < all; ++t) {
-      const float4 p = p4[t];
+      float v[E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float v = v1[t * Dp + 32 * i];
-        acc[0][i] = fmaf(p.x, v, acc[0][i]);
-        acc[1][i] = fmaf(p.y, v, acc[1][i]);
-        acc[2][i] = fmaf(p.z, v, acc[2][i]);
-        acc[3][i] = fmaf(p.w, v, acc[3][i]);
+      for (int i = 0; i < E; ++i) v[i] = v1[t * Dp + 32 * i];
+#pragma unroll
+      for (int r = 0; r < RW; r += 4) {
+        const float4 p = p4[(t * RW + r) / 4];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          acc[r][i] = fmaf(p.x, v[i], acc[r][i]);
+          acc[r + 1][i] = fmaf(p.y, v[i], acc[r + 1][i]);
+          acc[r + 2][i] = fmaf(p.z, v[i], acc[r + 2][i]);
+          acc[r + 3][i] = fmaf(p.w, v[i], acc[r + 3][i]);
+        }
       }
     }
     for (int t = all; t < any; ++t) {
@@ -279,24 +291,27 @@ void launch_merge(const AttnKv8Args& a, cudaStream_t s) {
   }
 }
 
-template <typename T, int E>
+template <typename T, int E, int RW>
 bool launch_split_e(const AttnKv8Args& a, cudaStream_t s) {
-  const size_t smem = split_smem(a.kv.D);
-  if (cudaFuncSetAttribute(attn_kv8_split_kernel<T, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess) {
+  const size_t smem = split_smem(a.kv.D, RW);
+  auto kernel = attn_kv8_split_kernel<T, E, RW>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     set_error("cudaFuncSetAttribute(attn_kv8_split_kernel) failed");
     return false;
   }
-  const int nrb = cdiv((long)a.K * (a.Hq / a.kv.Hkv), kRows);
+  const int nrb = row_blocks(a.K * (a.Hq / a.kv.Hkv), a.kv.D);
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)a.kv.D);
-  launch_pdl(attn_kv8_split_kernel<T, E>, dim3(a.n_splits, a.kv.Hkv * nrb, a.C), kThreads, smem, s, a, scale_log2);
+  launch_pdl(kernel, dim3(a.n_splits, a.kv.Hkv * nrb, a.C), kThreads, smem, s, a, scale_log2);
   note_launch();
   return true;
 }
 
 template <typename T>
 bool launch_split(const AttnKv8Args& a, cudaStream_t s) {
-  return a.kv.D <= 64 ? launch_split_e<T, 2>(a, s) : a.kv.D <= 128 ? launch_split_e<T, 4>(a, s) : launch_split_e<T, 8>(a, s);
+  const bool eight = rows_per_warp(a.K * (a.Hq / a.kv.Hkv), a.kv.D) == 8;
+  if (a.kv.D <= 64) return eight ? launch_split_e<T, 2, 8>(a, s) : launch_split_e<T, 2, 4>(a, s);
+  if (a.kv.D <= 128) return eight ? launch_split_e<T, 4, 8>(a, s) : launch_split_e<T, 4, 4>(a, s);
+  return launch_split_e<T, 8, 4>(a, s);
 }
 
 // CUDA-core path: tokens per split (a requested length, or about 16 CTAs per SM at the
@@ -306,7 +321,7 @@ struct Split {
 };
 Split split_of(int C, int K, int G, const Kv8& kv, int req) {
   const long max_keys = (long)kv.max_pages * kv.page_size + K;
-  const long nrb = cdiv((long)K * G, kRows);
+  const long nrb = row_blocks(K * G, kv.D);
   long per = req > 0 ? req : ((long)C * kv.Hkv * nrb * max_keys + 148L * 16 - 1) / (148L * 16);
   // A single tile where that gives every SM work enough (2 requests of 77 tokens: 9.9 us, 13.7
   // with two tiles); pairs of tiles otherwise (32 of 8192: 180 us in 256s, 194 in 224s).
@@ -343,7 +358,7 @@ bool attn_kv8(int dtype, AttnKv8Args& a, int split_req, void* ws, cudaStream_t s
   }
   const int G = a.Hq / a.kv.Hkv;
   const Split sp = split_of(a.C, a.K, G, a.kv, split_req);
-  if (a.C > 65535 || (long)a.kv.Hkv * cdiv((long)a.K * G, kRows) > 65535) {
+  if (a.C > 65535 || (long)a.kv.Hkv * row_blocks(a.K * G, a.kv.D) > 65535) {
     set_error("attention over the 8-bit cache: too many requests or heads");
     return false;
   }

@@ -246,6 +246,13 @@ def test_attention_query_rows(H, cuda, K, G):
     check_attention(H, cuda, [300, 70], K, 2 * G, 2, 64, 32, torch.bfloat16, False, False, seed=K + 1)
 
 
+@pytest.mark.parametrize("D", [64, 100, 128, 256])
+@pytest.mark.parametrize("K,G", [(8, 4), (11, 3), (16, 4), (13, 5), (29, 8)])
+def test_attention_query_rows_f32(H, cuda, K, G, D):
+    # 32 .. 232 query rows a kv head on the CUDA cores
+    check_attention(H, cuda, [100, 5, 0, 170], K, 2 * G, 2, D, 16, torch.float32, True, True, seed=K)
+
+
 @pytest.mark.parametrize("page", [80, 112, 144, 256, 1024])
 def test_attention_page_sizes(H, cuda, page):
     # tiles that begin inside pages, pages of several tiles
