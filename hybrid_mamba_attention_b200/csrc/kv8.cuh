@@ -41,12 +41,6 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
 }
 
-__device__ __forceinline__ uint32_t e4m3x2_h(__half2 v) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t*>(&v)));
-  return r;
-}
-
 // The two e4m3 codes in the low 16 bits of `r` as values (exact in fp16).
 __device__ __forceinline__ __half2 e4m3x2_to_h2(uint32_t r) {
   uint32_t h;
