@@ -318,16 +318,23 @@ bool launch_split(const AttnKv8Args& a, cudaStream_t s) {
 // table's full width) and splits per sequence.
 struct Split {
   int tokens, n;
+  int most;  // the most splits that a table of this width or a narrower one gives
 };
+constexpr long kSplitCtas = 148L * 16;
 Split split_of(int C, int K, int G, const Kv8& kv, int req) {
   const long max_keys = (long)kv.max_pages * kv.page_size + K;
-  const long nrb = row_blocks(K * G, kv.D);
-  long per = req > 0 ? req : ((long)C * kv.Hkv * nrb * max_keys + 148L * 16 - 1) / (148L * 16);
+  const long lines = (long)C * kv.Hkv * row_blocks(K * G, kv.D);
+  long per = req > 0 ? req : (lines * max_keys + kSplitCtas - 1) / kSplitCtas;
   // A single tile where that gives every SM work enough (2 requests of 77 tokens: 9.9 us, 13.7
   // with two tiles); pairs of tiles otherwise (32 of 8192: 180 us in 256s, 194 in 224s).
   per = per <= kTile ? kTile : (per + 2 * kTile - 1) / (2 * kTile) * (2 * kTile);
   // the grid's x extent holds the splits: no limit in reach (2^31), so any length works
-  return {(int)(per < max_keys ? per : max_keys), (int)((max_keys + per - 1) / per)};
+  const long n = (max_keys + per - 1) / per;
+  // The length is rounded up in steps, so a wider table may have fewer splits than a narrower
+  // one.  At any width a split has a tile at least and, unless its length is given, max_keys
+  // lines / kSplitCtas keys: both counts only grow with max_keys.
+  const long tiles = (max_keys + kTile - 1) / kTile, even = (kSplitCtas + lines - 1) / lines;
+  return {(int)(per < max_keys ? per : max_keys), (int)n, (int)(req > 0 ? n : tiles < even ? tiles : even)};
 }
 
 }  // namespace
@@ -339,7 +346,7 @@ bool attn_kv8_supported(int K, int G, int D, const char** why) {
   return true;
 }
 
-size_t attn_kv8_ws_bytes(int dtype, int C, int K, int Hq, const Kv8& kv, int split_req) {
+size_t attn_kv8_ws_bytes(int dtype, int C, int K, int Hq, const Kv8& kv, int split_req, bool narrower) {
   if (attn_kv8_tc_shape(dtype, kv.D, kv.page_size)) {
     AttnKv8Args a = {};
     a.kv = kv, a.C = C, a.K = K, a.Hq = Hq;
@@ -347,7 +354,7 @@ size_t attn_kv8_ws_bytes(int dtype, int C, int K, int Hq, const Kv8& kv, int spl
   }
   const int G = Hq / kv.Hkv;
   const Split sp = split_of(C, K, G, kv, split_req);
-  const size_t rows = (size_t)C * kv.Hkv * sp.n * K * G;
+  const size_t rows = (size_t)C * kv.Hkv * (narrower ? sp.most : sp.n) * K * G;
   return rows * (kv.D + 2) * sizeof(float);
 }
 

@@ -295,6 +295,15 @@ AttnKv8Args attn_kv8_args(const hspec_cfg* c, const hspec_kv8_view* kv, const in
   return a;
 }
 
+// Workspace of one attention call (0: refused); `narrower`: enough for every narrower table, too.
+size_t attn_kv8_ws(const hspec_cfg* c, int C, int K, int max_pages, bool narrower) {
+  if (validate_cfg(c, true, false) || C < 1 || K < 1 || K > 64 || max_pages < 1) return 0;
+  if ((long)max_pages * c->page_size > (1L << 30)) return 0;
+  hspec_kv8_view kv = {};
+  kv.max_pages = max_pages;
+  return align256(attn_kv8_ws_bytes(c->dtype, C, K, c->n_q_heads, kv8_of(c, &kv), c->attn_split_tokens, narrower));
+}
+
 struct AttnPlan {
   int split_tokens, n_splits, max_chunks;
   size_t rows;  // partial rows
@@ -388,7 +397,7 @@ StepPlan step_plan(const hspec_cfg* c, int C, int K, int max_pages, bool kv8) {
   s.h0 = off, off += align256(ssm && !step_fuses_inject(c) ? (size_t)C * HPN * 4 : 0);
   s.attn = off;
   if (att && kv8) {
-    off += hspec_attn_kv8_workspace_size(c, C, K, max_pages);
+    off += attn_kv8_ws(c, C, K, max_pages, true);  // (each layer's table may be narrower)
   } else if (att) {
     s.ap = attn_plan(c, C, K, max_pages);
     off += s.ap.ws;
@@ -638,11 +647,7 @@ hspec_status hspec_kv8_read(const hspec_cfg* cfg, const hspec_kv8_view* kv, cons
 }
 
 size_t hspec_attn_kv8_workspace_size(const hspec_cfg* cfg, int C, int K, int max_pages) {
-  if (validate_cfg(cfg, true, false) || C < 1 || K < 1 || K > 64 || max_pages < 1) return 0;
-  if ((long)max_pages * cfg->page_size > (1L << 30)) return 0;
-  hspec_kv8_view kv = {};
-  kv.max_pages = max_pages;
-  return align256(attn_kv8_ws_bytes(cfg->dtype, C, K, cfg->n_q_heads, kv8_of(cfg, &kv), cfg->attn_split_tokens));
+  return attn_kv8_ws(cfg, C, K, max_pages, false);
 }
 
 hspec_status hspec_attn_paged_block_kv8(const hspec_cfg* cfg, const void* q, const hspec_kv8_view* kv,

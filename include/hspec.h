@@ -385,7 +385,7 @@ HSPEC_API hspec_status hspec_draft_step(hspec_drafter* drafter, const hspec_step
  * attention layer, in order, and in->kv is not read.  Same shapes as hspec_draft_step, with
  * the attention's own (hspec_attn_paged_block_kv8); the block's keys and values stay in
  * cfg->dtype.  Workspace: hspec_step_kv8_workspace_size() bytes for the widest of the page
- * tables. */
+ * tables, which is enough for the narrower ones. */
 HSPEC_API size_t hspec_step_kv8_workspace_size(const hspec_cfg* cfg, int C, int K, int max_pages);
 HSPEC_API hspec_status hspec_draft_step_kv8(hspec_drafter* drafter, const hspec_step_in* in,
                                             const hspec_kv8_view* kv8, const hspec_step_out* out,
