@@ -360,22 +360,34 @@ bool attn_supported(int dtype, int K, int G, int D, const char** why) {
   return true;
 }
 
+// fp32 path: about 16 CTAs per SM at the table's full width, splits in steps of 64 tokens
+constexpr long kSplitCtas = 148L * 16, kSplitStep = 64;
+
 int attn_split_tokens(int dtype, int C, int Hkv, int K, int max_ctx, int requested) {
   // tensor-core path: the requested chunk length in tokens (whole 64-token units of the
   // partition's line), or 0
   // for one chunk per SM, chosen on the device from the actual context lengths
   if (dtype == HSPEC_DTYPE_BF16) return requested > 0 ? ((requested + 63) / 64) * 64 : 0;
   if (requested > 0) return requested;
-  const long target_ctas = 148L * 16;
-  long per = ((long)C * Hkv * (max_ctx + K) + target_ctas - 1) / target_ctas;
-  per = ((per + 63) / 64) * 64;
-  if (per < 64) per = 64;
+  long per = ((long)C * Hkv * (max_ctx + K) + kSplitCtas - 1) / kSplitCtas;
+  per = ((per + kSplitStep - 1) / kSplitStep) * kSplitStep;
+  if (per < kSplitStep) per = kSplitStep;
   return (int)per;
 }
 
 int attn_num_splits(int dtype, int K, int max_ctx, int split_tokens) {
   if (dtype == HSPEC_DTYPE_BF16) return 0;
   return (max_ctx + K + split_tokens - 1) / split_tokens;
+}
+
+int attn_most_splits(int dtype, int C, int Hkv, int K, int max_ctx, int requested) {
+  if (dtype == HSPEC_DTYPE_BF16 || requested > 0) return attn_num_splits(dtype, K, max_ctx, requested);
+  // a split has kSplitStep tokens at least, and (max_ctx + K) C Hkv / kSplitCtas: both counts
+  // only grow with max_ctx, the number of splits of a width itself does not (the length is
+  // rounded up in steps)
+  const long steps = ((long)max_ctx + K + kSplitStep - 1) / kSplitStep;
+  const long even = (kSplitCtas + (long)C * Hkv - 1) / ((long)C * Hkv);
+  return (int)(steps < even ? steps : even);
 }
 
 int attn_sub_splits(int dtype) { return dtype == HSPEC_DTYPE_BF16 ? 2 : 1; }

@@ -308,6 +308,7 @@ struct AttnPlan {
   int split_tokens, n_splits, max_chunks;
   size_t rows;  // partial rows
   size_t ws;
+  size_t ws_narrower;  // enough for every narrower table, too
 };
 
 AttnPlan attn_plan(const hspec_cfg* c, int C, int K, int max_pages) {
@@ -319,6 +320,8 @@ AttnPlan attn_plan(const hspec_cfg* c, int C, int K, int max_pages) {
   const int G = c->n_q_heads / c->n_kv_heads;
   p.rows = attn_partial_rows(c->dtype, C, c->n_kv_heads, K, G, p.n_splits, p.max_chunks);
   p.ws = align256(attn_ws_bytes(c->dtype, C, c->n_kv_heads, K, G, c->head_dim, p.n_splits, p.max_chunks));
+  const int most = attn_most_splits(c->dtype, C, c->n_kv_heads, K, max_ctx, c->attn_split_tokens);
+  p.ws_narrower = align256(attn_ws_bytes(c->dtype, C, c->n_kv_heads, K, G, c->head_dim, most, p.max_chunks));
   return p;
 }
 
@@ -368,7 +371,6 @@ bool step_fuses_inject(const hspec_cfg* c) {
 // Step workspace layout (all sub-buffers 256-byte aligned).
 struct StepPlan {
   size_t x, xn, big, y, g, h0, attn, pval, pidx, gpart, gcnt, rope, total;
-  AttnPlan ap;
   int n_parts;
   size_t gpart_bytes;  // partials of the projection / MLP GEMMs with a cut K loop
   int gmax_tiles;      // tile counters that follow them (per call site)
@@ -399,8 +401,7 @@ StepPlan step_plan(const hspec_cfg* c, int C, int K, int max_pages, bool kv8) {
   if (att && kv8) {
     off += attn_kv8_ws(c, C, K, max_pages, true);  // (each layer's table may be narrower)
   } else if (att) {
-    s.ap = attn_plan(c, C, K, max_pages);
-    off += s.ap.ws;
+    off += attn_plan(c, C, K, max_pages).ws_narrower;  // (each layer's table may be narrower)
   }
   const int head_rows = c->draft_vocab > 0 ? c->draft_vocab : c->vocab;
   s.n_parts = c->vocab > 0 ? cdiv(head_rows, argmax_tile_n(c->dtype)) : 0;

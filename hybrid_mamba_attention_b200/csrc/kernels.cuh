@@ -160,6 +160,8 @@ struct AttnArgs {
 // Split policy (tokens per split, splits per request) and workspace bytes.
 int attn_split_tokens(int dtype, int C, int Hkv, int K, int max_ctx, int requested);
 int attn_num_splits(int dtype, int K, int max_ctx, int split_tokens);
+// The most splits that a table of max_ctx tokens or a narrower one gives.
+int attn_most_splits(int dtype, int C, int Hkv, int K, int max_ctx, int requested);
 // Rows of partials (each D fp32 + (m, l)) and workspace bytes.
 size_t attn_partial_rows(int dtype, int C, int Hkv, int K, int G, int n_splits, int max_chunks);
 size_t attn_ws_bytes(int dtype, int C, int Hkv, int K, int G, int D, int n_splits, int max_chunks);

@@ -65,3 +65,19 @@ def test_kv8_tables_of_two_widths(H, cuda, sh):
     assert torch.isfinite(outs[0]).all()
     assert close(sh, outs[1], outs[0]) and close(sh, outs[2], outs[0])
     dr.close()
+
+
+def test_plain_tables_of_two_widths(H, cuda):
+    # the fp32 step over ordinary caches: its split length doubles at 2368 pages
+    lens = torch.tensor([2367 * 16, 2367 * 16 - 5], dtype=torch.int32, device=cuda)
+    st = I.make_step_inputs(I.Workload("w", F32, C=2, K=K, ctx_lo=2367 * 16, ctx_hi=2367 * 16, seed=0), cuda)
+    dr = H.Drafter(F32, st["weights"])
+    size = dr.workspace_size(2, K, 2368)
+    outs = []
+    for widths in ((2368, 2368), (2368, 2367), (2367, 2368)):
+        tables = [widened(c, w) for c, w in zip(st["kv"], widths)]
+        si = dr.step_in(2, K, st["h_last"], lens, tables, x_in=st["x_in"])
+        outs.append(run_step(H, cuda, F32, dr, size, lambda so, ws: dr.step(si, so, ws)))
+    assert torch.isfinite(outs[0]).all()
+    assert close(F32, outs[1], outs[0]) and close(F32, outs[2], outs[0])
+    dr.close()

@@ -36,3 +36,18 @@ def test_kv8_step_covers_narrower_tables(H, C, K, Hq, Hkv, D, page, split):
         c = cfg(H, dtype, Hq, Hkv, dim, page, split)
         check(lambda w: H.hspec_step_kv8_workspace_size(c, C, K, w),
               lambda w: H.hspec_attn_kv8_workspace_size(c, C, K, w))
+
+
+@pytest.mark.parametrize("split", [0, 64, 528])
+@pytest.mark.parametrize("C,K,Hq,Hkv,D,page", SHAPES)
+def test_step_covers_narrower_tables(H, C, K, Hq, Hkv, D, page, split):
+    for dtype in (H.HSPEC_DTYPE_F32, H.HSPEC_DTYPE_BF16):
+        c = cfg(H, dtype, Hq, Hkv, D, page, split)
+        check(lambda w: H.hspec_step_workspace_size(c, C, K, w), lambda w: H.hspec_attn_workspace_size(c, C, K, w))
+
+
+def test_attention_alone_needs_its_own_width_only(H):
+    # (the allocation-free entry point's fixed scratch takes what it took before)
+    c = cfg(H, H.HSPEC_DTYPE_F32, 4, 2, 64, 16)
+    a, b = H.hspec_attn_workspace_size(c, 2, 8, 2367), H.hspec_attn_workspace_size(c, 2, 8, 2368)
+    assert b < 0.6 * a and H.hspec_step_workspace_size(c, 2, 8, 2368) > a
