@@ -260,13 +260,26 @@ def _row_stride(rows, mate, D: int) -> int:
     st, shape = rows.stride(), rows.shape
     if shape != mate.shape or st != mate.stride() or st[2] != 1 or (st[1] != D and shape[1] != 1):
         raise ValueError("k and v rows must be [T, Hkv, D] of the same strides, each row dense")
+    if shape[0] > 1 and st[0] < shape[1] * shape[2]:  # (0 would stand for dense rows)
+        raise ValueError("k and v rows must not overlap (an expanded tensor's do)")
     return st[0] if shape[0] > 1 else 0
+
+
+def _rows(cfg: hspec_cfg, rows, mate, cu=None, first=None) -> int:
+    """The row stride of a write's or read's rows, which must be cfg's [T, Hkv, D]; first
+    has an entry for each of the C requests of cu [C + 1]."""
+    dtype = torch.bfloat16 if cfg.dtype == HSPEC_DTYPE_BF16 else torch.float32
+    if tuple(rows.shape[1:]) != (cfg.n_kv_heads, cfg.head_dim) or rows.dtype != dtype or mate.dtype != dtype:
+        raise ValueError(f"k and v rows must be [T, {cfg.n_kv_heads}, {cfg.head_dim}] of {dtype}")
+    if isinstance(first, torch.Tensor) and first.shape[0] + 1 < cu.shape[0]:
+        raise ValueError("first must have an entry per request")
+    return _row_stride(rows, mate, cfg.head_dim)
 
 
 def hspec_kv8_write(cfg: hspec_cfg, k_new, v_new, cu_new, first, kv: hspec_kv8_view, stream=None):
     """Quantises rows cu_new[c] .. cu_new[c + 1] - 1 of k_new, v_new [T, Hkv, D] (cfg dtype)
     into the 8-bit cache as tokens first[c], first[c] + 1, ... of request c."""
-    _check(_lib.hspec_kv8_write(ct.byref(cfg), _ptr(k_new), _ptr(v_new), _row_stride(k_new, v_new, cfg.head_dim),
+    _check(_lib.hspec_kv8_write(ct.byref(cfg), _ptr(k_new), _ptr(v_new), _rows(cfg, k_new, v_new, cu_new, first),
                                 _ptr(cu_new), _ptr(first), int(cu_new.shape[0]) - 1, int(k_new.shape[0]),
                                 ct.byref(kv), _stream(stream)), "hspec_kv8_write")
 
@@ -276,7 +289,7 @@ def hspec_kv8_read(cfg: hspec_cfg, kv: hspec_kv8_view, cu, first, k_out, v_out, 
     cu[c + 1] - 1 of k_out, v_out [T, Hkv, D] (cfg dtype)."""
     _check(_lib.hspec_kv8_read(ct.byref(cfg), ct.byref(kv), _ptr(cu), _ptr(first), int(cu.shape[0]) - 1,
                                int(k_out.shape[0]), _ptr(k_out), _ptr(v_out),
-                               _row_stride(k_out, v_out, cfg.head_dim), _stream(stream)), "hspec_kv8_read")
+                               _rows(cfg, k_out, v_out, cu, first), _stream(stream)), "hspec_kv8_read")
 
 
 def hspec_attn_kv8_workspace_size(cfg: hspec_cfg, C: int, K: int, max_pages: int) -> int:

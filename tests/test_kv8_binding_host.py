@@ -1,0 +1,62 @@
+"""CPU checks of what the Python binding of the 8-bit cache's write and read refuses: rows that
+the library would read past their ends (no GPU is touched here)."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def H():
+    from hybrid_mamba_attention_b200 import hspec
+    return hspec
+
+
+def cfg(H, Hkv, D, dtype=None):
+    return H.hspec_cfg(d_model=64, n_q_heads=Hkv, n_kv_heads=Hkv, head_dim=D, page_size=16, n_layers=1,
+                       layer_kinds=b"A", dtype=H.HSPEC_DTYPE_BF16 if dtype is None else dtype)
+
+
+def calls(H, c, rows, first=(0, 0)):
+    kv = H.hspec_kv8_view(k_codes=256, v_codes=256, k_scales=256, v_scales=256, num_pages=4, page_table=256, max_pages=4)
+    cu, first = torch.tensor([0, 1, 4], dtype=torch.int32), torch.tensor(first, dtype=torch.int32)
+    yield lambda: H.hspec_kv8_write(c, rows, rows, cu, first, kv, stream=0)
+    yield lambda: H.hspec_kv8_read(c, kv, cu, first, rows, rows, stream=0)
+
+
+def zeros(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("Hkv,D,rows", [
+    (2, 64, zeros(1, 2, 64).expand(4, 2, 64)),                       # one row for all: stride 0
+    (2, 64, zeros(512).as_strided((4, 2, 64), (64, 64, 1))),         # rows that overlap
+    (2, 64, zeros(4, 3, 64)), (3, 64, zeros(4, 2, 64)),              # other heads than the cache's
+    (1, 64, zeros(4, 1, 32)), (2, 64, zeros(4, 2, 128)),             # other head sizes
+    (1, 128, zeros(4, 256)[:, :64].unsqueeze(1)),                    # narrow rows of a wide tensor
+    (2, 64, zeros(4, 128)),                                          # not [T, Hkv, D]
+])
+def test_rows_of_other_shapes_are_refused(H, Hkv, D, rows):
+    n0 = H.hspec_launch_count()
+    for call in calls(H, cfg(H, Hkv, D), rows):
+        with pytest.raises(ValueError):
+            call()
+    assert H.hspec_launch_count() == n0
+
+
+def test_rows_of_another_type_and_short_starts_are_refused(H):
+    n0 = H.hspec_launch_count()
+    for c, rows, first in ((cfg(H, 2, 64, H.HSPEC_DTYPE_F32), zeros(4, 2, 64), (0, 0)),
+                           (cfg(H, 2, 64), torch.zeros(4, 2, 64), (0, 0)),
+                           (cfg(H, 2, 64), zeros(4, 2, 64), (0,))):
+        for call in calls(H, c, rows, first):
+            with pytest.raises(ValueError):
+                call()
+    assert H.hspec_launch_count() == n0
+
+
+def test_rows_that_are_fine(H):
+    c = cfg(H, 2, 64)
+    wide = zeros(4, 512)
+    for rows, stride in ((zeros(4, 2, 64), 128), (wide[:, 128:256].view(4, 2, 64), 512), (zeros(1, 2, 64), 0),
+                         (zeros(0, 2, 64), 0)):
+        assert H._rows(c, rows, rows) == stride
+    assert H._rows(cfg(H, 1, 64), wide[:, :64].unsqueeze(1), wide[:, 64:128].unsqueeze(1)) == 512
