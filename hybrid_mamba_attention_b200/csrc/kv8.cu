@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(const Kv8MoveArgs a
   __syncwarp();  // every lane has read the old scale
   if (lane == 0) *scale = now;
   // an old scale that is no power of two of this call's making is divided by as it is
-  const float inv = now == mine ? kv8_inverse(now) : now > 0.f ? fminf(1.f / now, 3.402823466e38f) : 0.f;
+  const float inv = now == mine ? kv8_inverse(now) : fminf(1.f / now, 3.402823466e38f);
   uint8_t* out = dst + (size_t)u.slot0 * D;
 #pragma unroll
   for (int j = 0; j < kHeld; ++j)

@@ -19,9 +19,10 @@ __device__ __forceinline__ float kv8_scale_of(float amax) {
   return __int_as_float(max(e, 1) << 23);
 }
 
-// 1 / s for a scale of kv8_scale_of (a normal power of two, so exact); 0 for s = 0.
+// 1 / s for a scale of kv8_scale_of (a normal power of two, so exact).  1 for s = 0, where the
+// finite values are zeros anyway and an infinity has to become the largest code, not 0 * inf.
 __device__ __forceinline__ float kv8_inverse(float s) {
-  return s > 0.f ? __int_as_float((254 << 23) - __float_as_int(s)) : 0.f;
+  return s > 0.f ? __int_as_float((254 << 23) - __float_as_int(s)) : 1.f;
 }
 
 // |v| for the scale's choice: infinities and NaN do not take part.
