@@ -38,7 +38,8 @@ struct Unit {
 __device__ __forceinline__ Unit find_unit(const Kv8MoveArgs& a, int u) {
   const int page = a.kv.page_size, lane = threadIdx.x & 31;
   Unit r = {0, 0, -1, 0};
-  // the last request whose slots start at or before u
+  // the last request whose slots start at or before u (with offsets that fall, the starts are not
+  // in order and the search may miss it: the slot's page is then left alone)
   int c = 0;
   for (int n = a.C; n > 1;) {
     const int step = (n + 31) / 32, i = lane * step;

@@ -266,8 +266,10 @@ typedef struct hspec_kv8_view {
  *   [cu_new[0], cu_new[C]) are not read);  first device [C] int32, tokens already cached.
  * A page may be written by one request's range only (pages that several requests share
  * must lie before every writer's first page); two ranges on one page leave codes of both
- * under one of their scales.  A bad cu_new pair, a range past max_pages * page_size or a
- * bad page id sets the device error word and writes nothing for that request or page.
+ * under one of their scales.  A cu_new pair outside 0 .. T, a range past max_pages *
+ * page_size or a bad page id sets the device error word and writes nothing for that request
+ * or page; the others are written.  Offsets that fall (cu_new[c] > cu_new[c+1]) set it, too,
+ * and then any page of any request of the call may be left as it was.
  * C >= 1, 0 <= T <= 2^30. */
 HSPEC_API hspec_status hspec_kv8_write(const hspec_cfg* cfg, const void* k_new, const void* v_new,
                                        long long row_stride, const int32_t* cu_new, const int32_t* first, int C,
