@@ -339,10 +339,16 @@ Split split_of(int C, int K, int G, const Kv8& kv, int req) {
 
 }  // namespace
 
-bool attn_kv8_supported(int K, int G, int D, const char** why) {
+bool attn_kv8_supported(int dtype, int C, int K, int Hq, const Kv8& kv, int split_req, const char** why) {
+  const long G = Hq / kv.Hkv;
   if (K < 1 || K > 64) return *why = "K must be in 1..64", false;
-  if (D > 256) return *why = "head_dim must be <= 256", false;
-  if ((long)K * G > 65536) return *why = "K * Hq / Hkv must be <= 65536", false;
+  if (kv.D > 256) return *why = "head_dim must be <= 256", false;
+  if (K * G > 65536) return *why = "K * Hq / Hkv must be <= 65536", false;
+  if (attn_kv8_tc_shape(dtype, kv.D, kv.page_size)) return attn_kv8_tc_fits(C, K, Hq, kv, split_req, why);
+  // the grid's y and z extents
+  if (C > 65535) return *why = "C must be <= 65535 off the tensor-core path", false;
+  if (kv.Hkv * (long)row_blocks((int)(K * G), kv.D) > 65535)
+    return *why = "more than 65535 kv heads times blocks of query rows", false;
   return true;
 }
 
@@ -365,10 +371,6 @@ bool attn_kv8(int dtype, AttnKv8Args& a, int split_req, void* ws, cudaStream_t s
   }
   const int G = a.Hq / a.kv.Hkv;
   const Split sp = split_of(a.C, a.K, G, a.kv, split_req);
-  if (a.C > 65535 || (long)a.kv.Hkv * row_blocks(a.K * G, a.kv.D) > 65535) {
-    set_error("attention over the 8-bit cache: too many requests or heads");
-    return false;
-  }
   a.split_tokens = sp.tokens, a.n_splits = sp.n;
   const size_t rows = (size_t)a.C * a.kv.Hkv * sp.n * a.K * G;
   a.ws_acc = (float*)ws;

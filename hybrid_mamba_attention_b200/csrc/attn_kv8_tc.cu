@@ -1289,21 +1289,24 @@ size_t attn_kv8_tc_plan(AttnKv8Args& a, int split_req, void* ws) {
   return off;
 }
 
+bool attn_kv8_tc_fits(int C, int K, int Hq, const Kv8& kv, int split_req, const char** why) {
+  AttnKv8Args a = {};
+  a.kv = kv, a.C = C, a.K = K, a.Hq = Hq;
+  attn_kv8_tc_plan(a, split_req, nullptr);
+  const double most = 2147483647.0, seqs = (double)C * kv.Hkv * a.n_rb;
+  // the line is indexed in 32 bits, with room for a chunk more
+  const long tiles = ((long)kv.max_pages * kv.page_size + TT - 1) / TT + 1;
+  if (seqs * (tiles + kAttn8SeqUnits) >= (double)(1 << 30))
+    return *why = "C * Hkv * blocks of 128 query rows * (table tokens / 128 + 5) must be below 2^30", false;
+  if ((double)kv.num_pages * kv.Hkv > most) return *why = "num_pages * Hkv must be below 2^31", false;
+  if ((double)C * kv.Hkv * (a.n_rb * a.row_block + 2.0 * blk_rows(K)) > most || (double)C * K * Hq > most ||
+      (seqs + a.max_chunks) * 2 * a.row_block > most)
+    return *why = "the query rows of the call must be below 2^30", false;
+  return true;
+}
+
 bool attn_kv8_tc_launch(AttnKv8Args& a, cudaStream_t s) {
   if (a.wait_ns == 0) a.wait_ns = tc::kWaitLimitNs;
-  // the line is indexed in 32 bits
-  const long tiles = ((long)a.kv.max_pages * a.kv.page_size + TT - 1) / TT + 1;
-  if ((double)a.C * a.kv.Hkv * a.n_rb * (tiles + kAttn8SeqUnits) >= (double)(1 << 30)) {
-    set_error("attention over the 8-bit cache: too many context tiles in one call");
-    return false;
-  }
-  const double rows = (double)a.C * a.kv.Hkv * (a.n_rb * a.row_block + 2.0 * blk_rows(a.K));
-  if ((double)a.kv.num_pages * a.kv.Hkv > 2147483647.0 || rows > 2147483647.0 ||
-      (double)a.C * a.K * a.Hq > 2147483647.0 ||
-      ((double)a.C * a.kv.Hkv * a.n_rb + a.max_chunks) * 2 * a.row_block > 2147483647.0) {
-    set_error("attention over the 8-bit cache: pool or batch too large");
-    return false;
-  }
   return a.kv.D == 128 ? launch_d<128>(a, s) : launch_d<64>(a, s);
 }
 

@@ -299,9 +299,12 @@ AttnKv8Args attn_kv8_args(const hspec_cfg* c, const hspec_kv8_view* kv, const in
 size_t attn_kv8_ws(const hspec_cfg* c, int C, int K, int max_pages, bool narrower) {
   if (validate_cfg(c, true, false) || C < 1 || K < 1 || K > 64 || max_pages < 1) return 0;
   if ((long)max_pages * c->page_size > (1L << 30)) return 0;
-  hspec_kv8_view kv = {};
-  kv.max_pages = max_pages;
-  return align256(attn_kv8_ws_bytes(c->dtype, C, K, c->n_q_heads, kv8_of(c, &kv), c->attn_split_tokens, narrower));
+  hspec_kv8_view v = {};
+  v.max_pages = max_pages;
+  const Kv8 kv = kv8_of(c, &v);
+  const char* why = "";
+  if (!attn_kv8_supported(c->dtype, C, K, c->n_q_heads, kv, c->attn_split_tokens, &why)) return 0;
+  return align256(attn_kv8_ws_bytes(c->dtype, C, K, c->n_q_heads, kv, c->attn_split_tokens, narrower));
 }
 
 struct AttnPlan {
@@ -663,7 +666,7 @@ hspec_status hspec_attn_paged_block_kv8(const hspec_cfg* cfg, const void* q, con
     FAIL(HSPEC_ERR_INVALID_ARG, "q, out, k_blk and v_blk must be 16-byte aligned");
   if (C < 1 || K < 1 || K > 64) FAIL(HSPEC_ERR_UNSUPPORTED, "C=%d K=%d (need C >= 1, 1 <= K <= 64)", C, K);
   const char* why = "";
-  if (!attn_kv8_supported(K, cfg->n_q_heads / cfg->n_kv_heads, cfg->head_dim, &why))
+  if (!attn_kv8_supported(cfg->dtype, C, K, cfg->n_q_heads, kv8_of(cfg, kv), cfg->attn_split_tokens, &why))
     FAIL(HSPEC_ERR_UNSUPPORTED, "attention over the 8-bit cache: %s", why);
   const size_t need = hspec_attn_kv8_workspace_size(cfg, C, K, kv->max_pages);
   if (!workspace || ((uintptr_t)workspace & 255) || ws_bytes < need)
@@ -756,7 +759,7 @@ size_t hspec_step_workspace_size(const hspec_cfg* cfg, int C, int K, int max_pag
 
 size_t hspec_step_kv8_workspace_size(const hspec_cfg* cfg, int C, int K, int max_pages) {
   if (!cfg || C < 1 || K < 1 || K > 64 || (has_kind(cfg, 'A') && max_pages < 1)) return 0;
-  if ((long)(max_pages > 0 ? max_pages : 1) * cfg->page_size > (1L << 30)) return 0;
+  if (has_kind(cfg, 'A') && !attn_kv8_ws(cfg, C, K, max_pages, true)) return 0;
   return step_plan(cfg, C, K, max_pages > 0 ? max_pages : 1, true).total;
 }
 
@@ -784,11 +787,14 @@ hspec_status draft_step(hspec_drafter* dr, const hspec_step_in* in, const hspec_
     if (!in->ctx_lens) FAIL(HSPEC_ERR_INVALID_ARG, "ctx_lens is NULL");
     const char* why = "";
     const int G = c->n_q_heads / c->n_kv_heads;
-    if (kv8s ? !attn_kv8_supported(K, G, c->head_dim, &why) : !attn_supported(c->dtype, K, G, c->head_dim, &why))
+    if (!kv8s && !attn_supported(c->dtype, K, G, c->head_dim, &why))
       FAIL(HSPEC_ERR_UNSUPPORTED, "attention: %s", why);
     for (int i = 0; i < c->n_layers; ++i) {
       if (c->layer_kinds[i] != 'A') continue;
       if ((st = kv8s ? validate_kv8(c, &kv8s[n_att]) : validate_kv(c, &in->kv[n_att]))) return st;
+      if (kv8s &&
+          !attn_kv8_supported(c->dtype, C, K, c->n_q_heads, kv8_of(c, &kv8s[n_att]), c->attn_split_tokens, &why))
+        FAIL(HSPEC_ERR_UNSUPPORTED, "attention over the 8-bit cache: %s", why);
       const int pages = kv8s ? kv8s[n_att].max_pages : in->kv[n_att].max_pages;
       if (pages > max_pages) max_pages = pages;
       ++n_att;

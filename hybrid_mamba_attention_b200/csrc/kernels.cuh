@@ -230,7 +230,9 @@ bool attn_kv8_tc_shape(int dtype, int D, int page_size);
 // Workspace bytes; sets the plan's fields of `a` (and with ws != NULL its pointers).
 size_t attn_kv8_tc_plan(AttnKv8Args& a, int split_req, void* ws);
 bool attn_kv8_tc_launch(AttnKv8Args& a, cudaStream_t s);
-bool attn_kv8_supported(int K, int G, int D, const char** why);
+// Whether a call can be launched (num_pages 0: not known yet).
+bool attn_kv8_supported(int dtype, int C, int K, int Hq, const Kv8& kv, int split_req, const char** why);
+bool attn_kv8_tc_fits(int C, int K, int Hq, const Kv8& kv, int split_req, const char** why);
 // For a page table of width kv.max_pages; `narrower`: enough for every narrower one, too.
 size_t attn_kv8_ws_bytes(int dtype, int C, int K, int Hq, const Kv8& kv, int split_req, bool narrower);
 // Fills the workspace fields and launches; false (message recorded) if it cannot.

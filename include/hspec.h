@@ -284,7 +284,7 @@ HSPEC_API hspec_status hspec_kv8_read(const hspec_cfg* cfg, const hspec_kv8_view
                                       long long row_stride, void* stream);
 
 /* Workspace bytes of hspec_attn_paged_block_kv8 for C requests of K query positions and a
- * page table of width max_pages. */
+ * page table of width max_pages; 0 for a size that the call refuses. */
 HSPEC_API size_t hspec_attn_kv8_workspace_size(const hspec_cfg* cfg, int C, int K, int max_pages);
 
 /* Paged in-place GQA attention over the 8-bit cache, scale 1/sqrt(D), in two forms:
@@ -310,7 +310,11 @@ HSPEC_API size_t hspec_attn_kv8_workspace_size(const hspec_cfg* cfg, int C, int 
  * q, out device [C, K, Hq, D] (dtype); k_blk, v_blk device [C, K, Hkv, D] (dtype) or both
  * NULL; ctx_lens device [C] int32; all of them and the codes 16-byte aligned; workspace
  * device, >= hspec_attn_kv8_workspace_size() bytes, 256-byte aligned.  C >= 1,
- * 1 <= K <= 64.  Calls on the same batch give bit-identical results. */
+ * 1 <= K <= 64, K * Hq / Hkv <= 65536.  Tensor-core path: C * Hkv * ceil(K * Hq / Hkv / 128) *
+ * (max_pages * page_size / 128 + 5) and the query rows C * K * Hq, rounded up to 32 a kv head,
+ * below 2^30, num_pages * Hkv below 2^31; CUDA cores: C <= 65535 and Hkv times the blocks of 32
+ * or 64 query rows <= 65535.  Larger sizes are refused (HSPEC_ERR_UNSUPPORTED) before anything
+ * is launched, by the draft step too.  Calls on the same batch give bit-identical results. */
 HSPEC_API hspec_status hspec_attn_paged_block_kv8(const hspec_cfg* cfg, const void* q, const hspec_kv8_view* kv,
                                                   const int32_t* ctx_lens, const void* k_blk, const void* v_blk,
                                                   int C, int K, void* out, void* workspace, size_t ws_bytes,
