@@ -153,9 +153,16 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# The current stream's raw handle, without a Stream object (which costs as much as the rest of a
+# call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    if stream is None:  # (the raw handle: a Stream object costs as much as the rest of a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -60,3 +60,15 @@ def test_rows_that_are_fine(H):
                          (zeros(0, 2, 64), 0)):
         assert H._rows(c, rows, rows) == stride
     assert H._rows(cfg(H, 1, 64), wide[:, :64].unsqueeze(1), wide[:, 64:128].unsqueeze(1)) == 512
+
+
+def test_current_stream_with_and_without_the_raw_handle(H, monkeypatch):
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(H, "_raw_stream", lambda device: 100 + device)
+    assert H._stream(None) == 103 and H._stream(5) == 5 and H._stream(Stream()) == 77
+    monkeypatch.setattr(H, "_raw_stream", None)
+    assert H._stream(None) == 77 and H._stream(5) == 5 and H._stream(Stream()) == 77
