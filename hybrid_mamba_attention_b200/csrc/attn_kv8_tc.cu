@@ -13,17 +13,21 @@
 // Rounding.  A bf16 query row is scaled by a power of two and held as two e4m3 parts,
 // hi + lo, which carry its 8 bits (down to 2^-17 of the row's largest element); both are
 // multiplied with K into one fp32 accumulator.  The weights p = 2^(s - m) <= 2^5 enter as
-// P = p * 2^3 * (V scale / largest V scale so far), hi = e4m3(P) and lo = e4m3(16 (P - hi))
-// side by side in one N = 2R product, O = O_hi + O_lo / 16: 8 bits down to 2^-9 of the
-// reference m, an absolute 2^-17 below.  Row sums use the unrounded fp32 weights.  The
+// P = p * 2^3 * (V scale / largest V scale so far), hi = e4m3(P) and lo = e4m3(32 (P - hi))
+// side by side in one N = 2R product, O = O_hi + O_lo / 32: 8 bits down to 2^-10 of the
+// reference m, an absolute 2^-18 below.  Row sums use the unrounded fp32 weights.  The
 // block's own bf16 keys and values are two e4m3 parts with a power-of-two scale per row, too.
 //
 // The reference m of a query starts as the first tile's maximum.  A tile's weights are
 // computed under the references so far, then checked: only where one exceeds 2^5 (or a V
 // scale the largest so far), which one barrier with an OR tells the group, the references
 // rise to the maxima, O and the sums are rescaled and the tile is weighed again.  They come
-// down, too, at a few marked items: the first key of a context outweighs the others as a
-// rule, and weights far below the reference have few bits.
+// down, too, where they are looked at: weights far below the reference have few bits, and a key
+// that outweighs all others (the first of a context does as a rule) would hide what follows.
+// That is a piece's second item, every 32nd from there on, and behind a rise by more than 2^8
+// the items 1, 5 and 21 on (a look costs about as much as an item: two more a piece, whatever
+// the data, made 128 requests of 64 columns 7 % slower each).  So at most 31 items' keys, each
+// below 2^-18, enter the sum and not O.
 //
 // Work partition: as the bf16 path's, the sequences (request, row block, kv head) lie end
 // to end on a line of units, kAttn8SeqUnits for a start and one per 128-key tile; the line
@@ -80,10 +84,11 @@ struct Warps {
 };
 constexpr float kPScale = 8.f;    // 2^3: weights enter P times this
 constexpr float kOver = 32.f;     // 2^5: a weight may reach this before the reference rises (P: 2^8 of e4m3's 448)
-constexpr float kSlack = 3.f;     // a reference over a tile's maximum by more than 2^3 comes down to that,
-constexpr float kBelow = 60.f;    // though not below 2^-60 of the largest score so far,
-constexpr int kSettle = 32;       // after a context's first tile and every 32 items
-constexpr float kLoScale = 16.f;  // the low part of P is held times this
+constexpr float kSlack = 3.f;     // where it is looked at, a reference over a tile's maximum by more than 2^3
+constexpr float kBelow = 60.f;    // comes down to that, though not below 2^-60 of the largest score so far
+constexpr int kSettle = 32;       // looked at in a piece's second item, then every 32; and from a rise on by more
+constexpr float kFar = 8.f;       // than 2^8 since the last look at gaps of 1, 4, 16, 32, ...
+constexpr float kLoScale = 32.f;  // the low part of P is held times this (the rest of up to 2^8 is 2^3 at most)
 constexpr int kMaxChunksAuto = 256, kMaxChunksExplicit = 2048;
 constexpr int kBlkRows = 64;      // scales of a block's rows (K <= 64)
 
@@ -111,7 +116,7 @@ struct Lay {
   static constexpr int STAGE = 2 * KV;
   static constexpr int P_BUF = TT * PN;                   // one byte an element
   static constexpr int OFF_Q = (2 * P_BUF + 1023) & ~1023;
-  static constexpr int MISC = 6144;
+  static constexpr int MISC = NR > 48 ? 6656 : 6144;
   // K/V ring stages beside nq query buffers
   static constexpr int stages(int nq) {
     const int room = (227 * 1024 - 1024 - MISC - OFF_Q - nq * Q_BUF) / STAGE;
@@ -142,7 +147,6 @@ enum : int {  // TileMeta::flags
   kQPar = 128,    // parity of the load into the piece's query buffer,
   kQShift = 8,    // whose number is in bits 8 and 9
   kHalf = 1024,   // odd tile of its piece
-  kSecond = 2048, // the same side's tile before was the context's first
 };
 struct alignas(16) TileMeta {  // written by producer warp 0 before the stage's barrier arrive
   int flags, cg, rb, slot;     // cg = request * Hkv + kv head; row block; the piece's slot
@@ -164,8 +168,10 @@ struct Misc {
   alignas(16) float nm[NG][NC];       // -reference (0 while there is none)
   alignas(16) float alpha[NG][NC];
   float m[NG][NC], top[NG][NC];       // the reference; the largest score so far
+  float base[NG][NC];                 // the reference when it was last looked at
   float cmax[NG][4][NC];              // per warp: column maxima, later the rows' sums
   float svmax[NG][4];
+  int look[NG], gap[NG];              // the item at which the references are looked at next; the gap before it
   uint4 v_nan[8];           // per stage: keys whose V row holds a NaN, as the groups find it
 };
 
@@ -324,9 +330,9 @@ __device__ __forceinline__ void split_weights(__half2 p0, __half2 p1, uint32_t& 
       "cvt.rn.satfinite.e4m3x2.f16x2 d, y;\n\t"
       "mov.b32 %1, {c, d};\n\t}\n"
       : "=&r"(hi), "=&r"(lo)
-      : "r"(*reinterpret_cast<uint32_t*>(&p0)), "r"(*reinterpret_cast<uint32_t*>(&p1)), "r"(0x4C004C00u));
+      : "r"(*reinterpret_cast<uint32_t*>(&p0)), "r"(*reinterpret_cast<uint32_t*>(&p1)), "r"(0x50005000u));
 }
-static_assert(kLoScale == 16.f, "0x4C00 is 16 in fp16");
+static_assert(kLoScale == 32.f, "0x5000 is 32 in fp16");
 
 // One lane of a converged warp (the tensor instructions are issued by it).
 __device__ __forceinline__ bool elect_one() {
@@ -547,7 +553,7 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           m.flags = (local == 0 ? kFirst : 0) | (local == n_tiles - 1 ? kLast : 0) | (local < STEP ? kGroupFirst : 0) |
                     (local >= n_tiles - STEP ? kGroupLast : 0) | (block ? kBlock : 0) |
                     (joff + valid - 1 > 0 ? kMixed : 0) | (quse & 1 ? kQPar : 0) | (qslot << kQShift) |
-                    (local & 1 ? kHalf : 0) | (pc.lt0 == 0 && local == STEP ? kSecond : 0);
+                    (local & 1 ? kHalf : 0);
           m.cg = pc.c * Hkv + g, m.rb = rb, m.slot = pc.c * spr + pc.r + pc.k, m.valid = valid, m.joff = joff;
           m.pad[0] = m.pad[1] = 0;
           ms.meta[s] = m;
@@ -812,7 +818,6 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       }
       over = fmaxf(top[0], top[1]);
     };
-    int since = 0;  // items of the piece so far
     int n = 0;      // items of the side so far
     int s = PAIR ? 0 : w;  // the item's stage
     for (;; ++n) {
@@ -843,15 +848,13 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
       }
       // The weights are 2^(s - reference), under the references so far; only if one exceeds
       // kOver (or a V scale the largest so far) do the references rise to the maxima and the
-      // tile's weights get computed again.  A piece's first tile has no references yet.  After
-      // a context's first tile, and every kSettle items, a reference far over the tile's own
-      // maximum comes down: the first key of a context outweighs, as a rule, any other, and
-      // weights far below the reference have few bits in P.  The side's last product must be done:
-      // its P buffer is free then, and O^T complete.
+      // tile's weights get computed again.  A piece's first tile has no references yet.  Where
+      // the references are looked at, one far over the tile's own maximum comes down: weights far
+      // below it have few bits in P.  The side's last product must be done: its P buffer is free
+      // then, and O^T complete.
       if (ok && n > 0) ok = wait(&ms.pv_done[w], (n - 1) & 1);
       if (ok && pend) write_partial();  // (before this item's product may overwrite it)
-      since = first ? 0 : since + 1;
-      const bool forced = first || (m.flags & kSecond) || (since & (kSettle - 1)) == 0;
+      const bool forced = first || n == ms.look[gq];
       bool weighed = false, moved = false, leave = false;
       while (true) {
         if (run && ok && (moved || !forced)) {
@@ -883,26 +886,36 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
           leave = true;
           break;
         }
-        if (quarter == 0)
+        if (quarter == 0) {
+          bool far = first;
           for (int j = lane; j < cols; j += 32) {
             const float cm =
                 fmaxf(fmaxf(ms.cmax[gq][0][j], ms.cmax[gq][1][j]), fmaxf(ms.cmax[gq][2][j], ms.cmax[gq][3][j]));
             const float m_old = first ? -INFINITY : ms.m[gq][j], top = first ? cm : fmaxf(ms.top[gq][j], cm);
             float m_new = fmaxf(m_old, cm);
             if (forced && cm > -INFINITY) m_new = fmaxf(fmaxf(cm, fminf(m_old, cm + kSlack)), top - kBelow);
+            const bool up = first || m_new - ms.base[gq][j] > kFar;
+            if (up || forced) ms.base[gq][j] = m_new;
+            far = far || up;
             ms.m[gq][j] = m_new;
             ms.top[gq][j] = top;
             if (first) cqs[j] = cq[j];
             nms[j] = m_new == -INFINITY ? 0.f : -m_new;
             alpha[j] = m_old == -INFINITY ? 1.f : exp2f(m_old - m_new);
           }
+          far = __any_sync(0xffffffffu, far);
+          if (lane == 0 && (far || forced)) {
+            ms.gap[gq] = first ? kSettle / 4 : far ? 1 : min(ms.gap[gq] * 4, kSettle);
+            ms.look[gq] = n + (far ? 1 : ms.gap[gq]);
+          }
+        }
         const float sv_top = fmaxf(fmaxf(ms.svmax[gq][0], ms.svmax[gq][1]), fmaxf(ms.svmax[gq][2], ms.svmax[gq][3]));
         // (at least the smallest normal number: its inverse is finite)
         const float mv_new = fmaxf(first ? sv_top : fmaxf(Mv, sv_top), 1.17549435e-38f);
         const float mv_ratio = Mv / mv_new;
         Mv = mv_new;
         inv_mv = 1.f / Mv;
-        group_or(false);  // cq, nm, m and alpha are written
+        group_or(false);  // cq, nm, m, alpha and look are written
         if (first) {
 #pragma unroll
           for (int j = 0; j < NC / 2; ++j) l2[j] = 0;

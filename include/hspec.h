@@ -298,11 +298,14 @@ HSPEC_API size_t hspec_attn_kv8_workspace_size(const hspec_cfg* cfg, int C, int 
  * Cached values enter as the exact code * scale of their page.  On the tensor-core path
  * (bf16, D = 64 or 128, page_size a multiple of 16):
  *  - the softmax weights enter the product with V as two e4m3 parts, 8 significant bits for
- *    weights down to 2^-9 of a running reference and 2^-17 of it as the error of smaller ones
- *    (the reference is a recent maximum of the row: it leaves out a context's first
- *    keys, and comes down again behind other keys that outweigh all around them), and fewer
- *    where a page's V scale is far below the largest of the request and head, a bit for
- *    each factor of two beyond 2^-9;
+ *    weights down to 2^-10 of a running reference and 2^-18 of it as the error of smaller ones
+ *    (the reference is a recent maximum of the row: it comes down again within a tile or two
+ *    behind keys that outweigh all others, a context's first among them), and fewer where a
+ *    page's V scale is far below the largest of the request and head, a bit for each factor of
+ *    two beyond 2^-10.  The errors have no sign of their own, but weights below 2^-18 are lost
+ *    from the output and not from the sum it is divided by: some 2^-10 of the largest weight
+ *    behind a single key that outweighs the others, 2^-6 at worst (thousands of keys just
+ *    below 2^-18 behind a few in such a spacing that each look at the reference meets one);
  *  - an infinity or NaN among the query, block key or block value elements enters as NaN;
  *  - a NaN in the values of one of the last K tokens, or in the block's when the flag hides
  *    some of it, makes every element of the rows that see it NaN.
