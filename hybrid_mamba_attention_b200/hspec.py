@@ -263,40 +263,49 @@ def hspec_attn_paged_block_noalloc(cfg: hspec_cfg, q, kv: hspec_kv_view, ctx_len
 
 def _row_stride(rows, mate, D: int) -> int:
     """Elements between the rows of [T, Hkv, D] tensors (a slice of a wider projection's
-    output will do), each row's heads dense."""
+    output will do), each row's heads dense and no row over another."""
     st, shape = rows.stride(), rows.shape
-    if shape != mate.shape or st != mate.stride() or st[2] != 1 or (st[1] != D and shape[1] != 1):
+    row, head, dim = st
+    if shape != mate.shape or st != mate.stride() or dim != 1 or (head != D and shape[1] != 1):
         raise ValueError("k and v rows must be [T, Hkv, D] of the same strides, each row dense")
-    if shape[0] > 1 and st[0] < shape[1] * shape[2]:  # (0 would stand for dense rows)
-        raise ValueError("k and v rows must not overlap (an expanded tensor's do)")
-    return st[0] if shape[0] > 1 else 0
+    T, heads, dims = shape
+    if T < 2:
+        return 0
+    if row < heads * dims:  # (an expanded tensor's 0 would stand for dense rows)
+        raise ValueError("k and v rows must not overlap")
+    return row
 
 
-def _rows(cfg: hspec_cfg, rows, mate, cu=None, first=None) -> int:
-    """The row stride of a write's or read's rows, which must be cfg's [T, Hkv, D]; first
-    has an entry for each of the C requests of cu [C + 1]."""
-    dtype = torch.bfloat16 if cfg.dtype == HSPEC_DTYPE_BF16 else torch.float32
-    if tuple(rows.shape[1:]) != (cfg.n_kv_heads, cfg.head_dim) or rows.dtype != dtype or mate.dtype != dtype:
+_DTYPES = {HSPEC_DTYPE_F32: torch.float32, HSPEC_DTYPE_BF16: torch.bfloat16}
+
+
+def _rows(cfg: hspec_cfg, rows, mate, cu, first):
+    """(C, T, row stride) of a write's or read's rows, which must be cfg's [T, Hkv, D]; first has
+    an entry for each of the C requests of cu [C + 1]."""
+    T, heads, dims = rows.shape
+    dtype = _DTYPES.get(cfg.dtype)  # (a cfg of another dtype is the library's to refuse)
+    if heads != cfg.n_kv_heads or dims != cfg.head_dim or dtype and not rows.dtype is mate.dtype is dtype:
         raise ValueError(f"k and v rows must be [T, {cfg.n_kv_heads}, {cfg.head_dim}] of {dtype}")
-    if isinstance(first, torch.Tensor) and first.shape[0] + 1 < cu.shape[0]:
+    C = cu.numel() - 1
+    if first is not None and not isinstance(first, int) and first.numel() < C:
         raise ValueError("first must have an entry per request")
-    return _row_stride(rows, mate, cfg.head_dim)
+    return C, T, _row_stride(rows, mate, dims)
 
 
 def hspec_kv8_write(cfg: hspec_cfg, k_new, v_new, cu_new, first, kv: hspec_kv8_view, stream=None):
     """Quantises rows cu_new[c] .. cu_new[c + 1] - 1 of k_new, v_new [T, Hkv, D] (cfg dtype)
     into the 8-bit cache as tokens first[c], first[c] + 1, ... of request c."""
-    _check(_lib.hspec_kv8_write(ct.byref(cfg), _ptr(k_new), _ptr(v_new), _rows(cfg, k_new, v_new, cu_new, first),
-                                _ptr(cu_new), _ptr(first), int(cu_new.shape[0]) - 1, int(k_new.shape[0]),
-                                ct.byref(kv), _stream(stream)), "hspec_kv8_write")
+    C, T, stride = _rows(cfg, k_new, v_new, cu_new, first)
+    _check(_lib.hspec_kv8_write(ct.byref(cfg), k_new.data_ptr(), v_new.data_ptr(), stride, cu_new.data_ptr(),
+                                _ptr(first), C, T, ct.byref(kv), _stream(stream)), "hspec_kv8_write")
 
 
 def hspec_kv8_read(cfg: hspec_cfg, kv: hspec_kv8_view, cu, first, k_out, v_out, stream=None):
     """Reads tokens first[c] .. of request c (first None: from 0) into rows cu[c] ..
     cu[c + 1] - 1 of k_out, v_out [T, Hkv, D] (cfg dtype)."""
-    _check(_lib.hspec_kv8_read(ct.byref(cfg), ct.byref(kv), _ptr(cu), _ptr(first), int(cu.shape[0]) - 1,
-                               int(k_out.shape[0]), _ptr(k_out), _ptr(v_out),
-                               _rows(cfg, k_out, v_out, cu, first), _stream(stream)), "hspec_kv8_read")
+    C, T, stride = _rows(cfg, k_out, v_out, cu, first)
+    _check(_lib.hspec_kv8_read(ct.byref(cfg), ct.byref(kv), cu.data_ptr(), _ptr(first), C, T, k_out.data_ptr(),
+                               v_out.data_ptr(), stride, _stream(stream)), "hspec_kv8_read")
 
 
 def hspec_attn_kv8_workspace_size(cfg: hspec_cfg, C: int, K: int, max_pages: int) -> int:

@@ -58,8 +58,8 @@ def test_rows_that_are_fine(H):
     wide = zeros(4, 512)
     for rows, stride in ((zeros(4, 2, 64), 128), (wide[:, 128:256].view(4, 2, 64), 512), (zeros(1, 2, 64), 0),
                          (zeros(0, 2, 64), 0)):
-        assert H._rows(c, rows, rows) == stride
-    assert H._rows(cfg(H, 1, 64), wide[:, :64].unsqueeze(1), wide[:, 64:128].unsqueeze(1)) == 512
+        assert H._rows(c, rows, rows, torch.zeros(3), torch.zeros(2)) == (2, rows.shape[0], stride)
+    assert H._rows(cfg(H, 1, 64), wide[:, :64].unsqueeze(1), wide[:, 64:128].unsqueeze(1), torch.zeros(1), None) == (0, 4, 512)
 
 
 def test_current_stream_with_and_without_the_raw_handle(H, monkeypatch):
