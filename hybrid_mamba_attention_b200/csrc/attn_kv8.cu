@@ -4,7 +4,7 @@
 // attn_kv8_split_kernel: one CTA per (split, kv head g and block of 32 or 64 query rows,
 // request c).  Its rows are (position j, query head g*G + i) pairs, all reading kv head
 // g.  Keys and values pass through shared memory in tiles of 32, dequantised to fp32
-// (code * scale is exact there); a warp owns four rows or eight: lane t computes their dot
+// (code * scale is exact there for the write's powers of two); a warp owns four rows or eight: lane t computes their dot
 // products with key t, the online softmax (exp2 domain) reduces over the lanes, and for
 // the product with V a lane owns the dims t, t + 32, ...  Hidden keys are skipped, not
 // multiplied by zero, so that a NaN in one reaches no row that does not see it.

@@ -295,7 +295,8 @@ HSPEC_API size_t hspec_attn_kv8_workspace_size(const hspec_cfg* cfg, int C, int 
  *    already): query j sees all ctx_lens[c] cached tokens, or with
  *    HSPEC_FLAG_CAUSAL_BLOCK those before position ctx_lens[c] - (K - 1) + j.  A query
  *    that sees none gives zeros.
- * Cached values enter as the exact code * scale of their page.  On the tensor-core path
+ * Cached values enter as code * scale of their page (a product in fp32, exact for the scales
+ * that hspec_kv8_write chooses).  On the tensor-core path
  * (bf16, D = 64 or 128, page_size a multiple of 16):
  *  - the softmax weights enter the product with V as two e4m3 parts, 8 significant bits for
  *    weights down to 2^-10 of a running reference and 2^-18 of it as the error of smaller ones
