@@ -171,6 +171,8 @@ struct Misc {
   float base[NG][NC];                 // the reference when it was last looked at
   float cmax[NG][4][NC];              // per warp: column maxima, later the rows' sums
   float svmax[NG][4];
+  int pend_base[NG], pend_rows[NG];   // the partial that O^T still holds
+  float pend_mul[NG];
   int look[NG], gap[NG];              // the item at which the references are looked at next; the gap before it
   uint4 v_nan[8];           // per stage: keys whose V row holds a NaN, as the groups find it
 };
@@ -741,13 +743,13 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
     bool ok = true;
     // the previous piece's partial, still in O^T
     bool pend = false;
-    int pend_base = 0, pend_rows = 0;
-    float pend_mul = 0.f;
     // O^T (every product issued into it has finished) to the workspace
     auto write_partial = [&]() {
       tc::tc_fence_after();
       const int d = D == 128 ? key : quarter * 16 + lane;
       const bool on = D == 128 || lane < 16;
+      const int pend_base = ms.pend_base[gq], pend_rows = ms.pend_rows[gq];
+      const float pend_mul = ms.pend_mul[gq];
 #pragma unroll 1
       for (int j0 = 0; j0 < pend_rows; j0 += 8) {
         float hi[8], lo[8];
@@ -1062,9 +1064,10 @@ __global__ void __launch_bounds__(Warps<NR>::THREADS, 1)
             ml[0] = ms.m[gq][j];
             ml[1] = (ms.cmax[gq][0][j] + ms.cmax[gq][1][j]) + (ms.cmax[gq][2][j] + ms.cmax[gq][3][j]);
           }
-        group_or(false);  // cmax and m may be written again
-        pend = true, pend_base = base, pend_rows = rows;
-        pend_mul = Mv * (1.f / kPScale);
+        if (quarter == 0 && lane == 0)
+          ms.pend_base[gq] = base, ms.pend_rows[gq] = rows, ms.pend_mul[gq] = Mv * (1.f / kPScale);
+        group_or(false);  // cmax and m may be written again, the partial's place is there
+        pend = true;
       }
       s += PAIR ? 1 : 2;
       if (s >= NS) s -= NS;
