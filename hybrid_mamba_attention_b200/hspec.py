@@ -192,9 +192,16 @@ def kv_view(cache: dict) -> hspec_kv_view:
                          max_pages=int(cache["page_table"].shape[1]))
 
 
+_KV8_FIELDS = (("k_codes", 1), ("v_codes", 1), ("k_scales", 4), ("v_scales", 4), ("page_table", 4))
+
+
 def kv8_view(cache: dict) -> hspec_kv8_view:
     """hspec_kv8_view of an 8-bit cache dict: k_codes, v_codes [num_pages, Hkv, page, D]
-    (one byte each), k_scales, v_scales [num_pages, Hkv] fp32, page_table."""
+    (one byte each), k_scales, v_scales [num_pages, Hkv] fp32, page_table int32; all contiguous."""
+    for name, size in _KV8_FIELDS:
+        t = cache[name]
+        if isinstance(t, torch.Tensor) and not (t.is_contiguous() and t.element_size() == size):
+            raise ValueError(f"{name} must be contiguous with elements of {size} bytes")
     return hspec_kv8_view(k_codes=_ptr(cache["k_codes"]), v_codes=_ptr(cache["v_codes"]),
                           k_scales=_ptr(cache["k_scales"]), v_scales=_ptr(cache["v_scales"]),
                           num_pages=int(cache["k_codes"].shape[0]), page_table=_ptr(cache["page_table"]),
@@ -312,14 +319,26 @@ def hspec_attn_kv8_workspace_size(cfg: hspec_cfg, C: int, K: int, max_pages: int
     return int(_lib.hspec_attn_kv8_workspace_size(ct.byref(cfg), C, K, max_pages))
 
 
+def _dense(t, n: int, dtype) -> bool:
+    """t (None and raw pointers pass) is n contiguous elements of dtype."""
+    return t is None or isinstance(t, int) or t.numel() == n and t.is_contiguous() and (
+        t.dtype is dtype or dtype is None)
+
+
 def hspec_attn_paged_block_kv8(cfg: hspec_cfg, q, kv: hspec_kv8_view, ctx_lens, k_blk, v_blk, out, workspace,
                                stream=None):
-    """Block attention over the 8-bit cache; k_blk = v_blk = None: over the cache alone."""
-    C, K = int(q.shape[0]), int(q.shape[1])
-    _check(_lib.hspec_attn_paged_block_kv8(ct.byref(cfg), _ptr(q), ct.byref(kv), _ptr(ctx_lens), _ptr(k_blk),
-                                           _ptr(v_blk), C, K, _ptr(out), _ptr(workspace),
-                                           workspace.numel() * workspace.element_size(), _stream(stream)),
-           "hspec_attn_paged_block_kv8")
+    """Block attention over the 8-bit cache; k_blk = v_blk = None: over the cache alone.  q and out
+    [C, K, Hq, D], k_blk and v_blk [C, K, Hkv, D], contiguous, of cfg's dtype."""
+    C, K = q.shape[:2]
+    n, dtype = C * K * cfg.head_dim, _DTYPES.get(cfg.dtype)
+    bad = not (_dense(q, n * cfg.n_q_heads, dtype) and _dense(out, n * cfg.n_q_heads, dtype))
+    if k_blk is not None or v_blk is not None:
+        bad = bad or not (_dense(k_blk, n * cfg.n_kv_heads, dtype) and _dense(v_blk, n * cfg.n_kv_heads, dtype))
+    if bad or not isinstance(ctx_lens, int) and ctx_lens.numel() < C:
+        raise ValueError("q, out, k_blk and v_blk must be contiguous, of cfg's heads and dtype, ctx_lens of C entries")
+    _check(_lib.hspec_attn_paged_block_kv8(ct.byref(cfg), q.data_ptr(), ct.byref(kv), _ptr(ctx_lens), _ptr(k_blk),
+                                           _ptr(v_blk), C, K, _ptr(out), workspace.data_ptr(), workspace.nbytes,
+                                           _stream(stream)), "hspec_attn_paged_block_kv8")
 
 
 def hspec_drafter_create(cfg: hspec_cfg, weights: hspec_model_weights) -> ct.c_void_p:
