@@ -46,10 +46,11 @@
 //
 // What bounds it, at 32 query and 8 KV heads of 128 dims but for the first: few columns HBM,
 // 2 D bytes a key and kv head (64 requests of 1024 .. 32768 tokens, 64 query heads, one
-// position: 370 .. 390 us, 5.7 .. 6.0 TB/s of the 6.56 that a copy reaches); with more, the
-// instructions that turn S^T into P, some 14 a weight of which six split it in two parts (128
-// requests of 512 .. 16384 tokens, 16 positions: 830 us, 2.7 TB/s; prepare 25 and merge 34 of
-// them); single requests the three kernels' latencies (512 tokens: 16 us; prepare 4, this 9,
+// position: 363 .. 390 us, 5.7 .. 6.1 TB/s of the 6.56 that a copy reaches); with more, the
+// chain that turns S^T into P and its latency: 27 instructions issued a weight in all warps, about
+// nine of them in weighing and three of those its split in two parts, 0.6 of the issue slots (128
+// requests of 512 .. 16384 tokens, 16 positions: 800 us in a burst, 830 .. 890 back to back under
+// the power cap, 2.7 TB/s; prepare 25 and merge 34 of them); single requests the three kernels' latencies (512 tokens: 16 us; prepare 4, this 9,
 // merge 4).  Every wait gives up after a time bound and sets the device error word.
 #include <stdint.h>
 

@@ -16,7 +16,7 @@
 // bf16, pages of 16: 16 prefixes of 512 .. 8192 tokens are read in 78 us (5.5 TB/s of the 6.56
 // that a copy reaches), 8 prompts of 512 .. 16384 written in 88 us (4.7 TB/s: one warp waits
 // for its page's rows, finds their maximum and only then stores), a token of each of 128
-// requests in 7.0 us, a launch and four loads one after the other.
+// requests in 7.2 us, a launch and four loads one after the other; fp32: 154, 129 and 7.8 us.
 #include <type_traits>
 
 #include "../../include/hspec.h"
